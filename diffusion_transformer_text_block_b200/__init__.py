@@ -58,6 +58,17 @@ class SampleOptions(ctypes.Structure):
                 ("change_out", ctypes.POINTER(ctypes.c_float))]
 
 
+class QkNormRopeArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32)] + [(n, ctypes.c_int32) for n in (
+        "in_dtype", "out_dtype", "rows", "heads_q", "heads_k", "head_dim", "rot_dim", "pairing", "n_pos")] + [
+        ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)] + [(n, ctypes.c_int64) for n in (
+            "q_stride", "k_stride", "q_out_stride", "k_out_stride")] + [(n, ctypes.c_void_p) for n in (
+                "q", "k", "q_out", "k_out", "q_gain", "k_gain", "rope", "positions")]
+
+
+DTYPE_F32, DTYPE_BF16 = 0, 1
+ROPE_PAIRINGS = {"adjacent": 0, "halves": 1}
+
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -99,6 +110,13 @@ _SIGS = {
     "moss_op_attention": (_I, [_P, _P, _I, _I, _I, _P]),
     "moss_op_ln_modulate": (_I, [_P, _P, _P, _P, _I, _I, _P]),
     "moss_op_modulation": (_I, [_P, _F, _P, _P]),
+    "moss_op_quantize_i8": (_I, [_P, _I, _I64, _P, _P, _I, _I, _P]),
+    "moss_op_ln_modulate_i8": (_I, [_P, _P, _P, _P, _P, _I, _I, _P]),
+    "moss_op_swiglu_i8": (_I, [_P, _I64, _P, _P, _I, _I, _P]),
+    "moss_op_gemm_i8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "moss_qk_norm_rope_args_init": (None, [ctypes.POINTER(QkNormRopeArgs), ctypes.c_uint32]),
+    "moss_op_qk_norm_rope": (_I, [ctypes.POINTER(QkNormRopeArgs), _P]),
+    "moss_op_rope_table": (_I, [_P, _I, _I, _I, _P]),
     "moss_modulation_noalloc": (_I, [ctypes.POINTER(Config), ctypes.POINTER(Weights), ctypes.POINTER(_F), _I, _P,
                                      _P]),
 }
@@ -246,6 +264,179 @@ def op_ln_modulate(x, shift, scale, stream=None):
     _check(lib().moss_op_ln_modulate(_ptr(x, f, "x"), _ptr(shift, f, "shift"), _ptr(scale, f, "scale"),
                                      h.data_ptr(), rows, dim, _stream(stream)))
     return h
+
+
+# ----------------------------------------------------------------------------- the 8-bit linear path
+def _on_current_device(**tensors):
+    """The library launches on the current device: refuse tensors of another one (or of the host)."""
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise MossError(1, f"{name} must be a CUDA tensor")
+        if t.device.index != dev:
+            raise MossError(1, f"{name} is on cuda:{t.device.index}, not on the current device cuda:{dev}")
+
+
+def _dtype_code(t, name):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return DTYPE_BF16
+    if t.dtype == torch.float32:
+        return DTYPE_F32
+    raise MossError(1, f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+
+
+def _rows_of(t, name):
+    """(rows, width, stride between rows) of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise MossError(1, f"{name} must be [rows, dim] with contiguous rows")
+    return t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _shaped(t, shape, dtype, name):
+    """A contiguous tensor of this shape and type, as a pointer (None stays None)."""
+    if t is not None and tuple(t.shape) != shape:
+        raise MossError(1, f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return _ptr(t, dtype, name)
+
+
+def op_quantize_i8(x, stream=None):
+    """Rows of x [rows, dim] (BF16 or FP32; rows may lie apart) to (q int8 [rows, dim], scale FP32
+    [rows]): q = round(127 x / amax), halves to even, scale = amax / 127."""
+    import torch
+    _on_current_device(x=x)
+    code = _dtype_code(x, "x")
+    rows, dim, stride = _rows_of(x, "x")
+    q = torch.empty(rows, dim, device=x.device, dtype=torch.int8)
+    scale = torch.empty(rows, device=x.device, dtype=torch.float32)
+    _check(lib().moss_op_quantize_i8(x.data_ptr(), code, stride, q.data_ptr(), scale.data_ptr(), rows, dim,
+                                     _stream(stream)))
+    return q, scale
+
+
+def op_ln_modulate_i8(x, shift, scale, stream=None):
+    """LN(x) (1 + scale) + shift of FP32 x [rows, dim], made 8-bit by rows: (q int8, q_scale FP32 [rows])."""
+    import torch
+    _on_current_device(x=x, shift=shift, scale=scale)
+    rows, dim = x.shape
+    f = torch.float32
+    q = torch.empty(rows, dim, device=x.device, dtype=torch.int8)
+    q_scale = torch.empty(rows, device=x.device, dtype=f)
+    _check(lib().moss_op_ln_modulate_i8(_ptr(x, f, "x"), _shaped(shift, (dim,), f, "shift"),
+                                        _shaped(scale, (dim,), f, "scale"), q.data_ptr(), q_scale.data_ptr(), rows,
+                                        dim, _stream(stream)))
+    return q, q_scale
+
+
+def op_swiglu_i8(gu, stream=None):
+    """SiLU(g) * u of BF16 gu [rows, 2 dim] (each row g | u; rows may lie apart), made 8-bit by rows:
+    (q int8 [rows, dim], scale FP32 [rows])."""
+    import torch
+    _on_current_device(gu=gu)
+    if gu.dtype != torch.bfloat16:
+        raise MossError(1, f"gu must be torch.bfloat16, got {gu.dtype}")
+    rows, width, stride = _rows_of(gu, "gu")
+    if width % 2:
+        raise MossError(1, "gu must hold gate and up halves of one width")
+    q = torch.empty(rows, width // 2, device=gu.device, dtype=torch.int8)
+    scale = torch.empty(rows, device=gu.device, dtype=torch.float32)
+    _check(lib().moss_op_swiglu_i8(gu.data_ptr(), stride, q.data_ptr(), scale.data_ptr(), rows, width // 2,
+                                   _stream(stream)))
+    return q, scale
+
+
+def op_gemm_i8(a, a_scale, b, b_scale, bias=None, gate=None, residual=None, out_dtype=None, out=None, stream=None):
+    """(A B^T) a_scale[:, None] b_scale + bias of int8 A [M, K] and B [N, K], BF16 unless out_dtype or out
+    says FP32; with gate [N] and residual [M, N] (FP32): residual + gate * that, in FP32.  out may be the
+    residual."""
+    import torch
+    _on_current_device(a=a, a_scale=a_scale, b=b, b_scale=b_scale, bias=bias, gate=gate, residual=residual, out=out)
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+        raise MossError(1, "a must be [M, K] and b [N, K]")
+    M, K = a.shape
+    N = b.shape[0]
+    f = torch.float32
+    if out is None:
+        out = torch.empty(M, N, device=a.device,
+                          dtype=out_dtype or (f if residual is not None else torch.bfloat16))
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise MossError(1, f"out is {out.dtype}, not {out_dtype}")
+    _check(lib().moss_op_gemm_i8(
+        _ptr(a, torch.int8, "a"), _shaped(a_scale, (M,), f, "a_scale"), _ptr(b, torch.int8, "b"),
+        _shaped(b_scale, (N,), f, "b_scale"), _shaped(bias, (N,), torch.bfloat16, "bias"),
+        _shaped(gate, (N,), f, "gate"), _shaped(residual, (M, N), f, "residual"), _shaped(out, (M, N), None, "out"),
+        _dtype_code(out, "out"), M, N, K, _stream(stream)))
+    return out
+
+
+def _heads_of(t, name):
+    """(rows, heads, head_dim, stride between tokens) of [rows, heads, head_dim] with packed heads."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise MossError(1, f"{name} must be [tokens, heads, head_dim] with each token's heads contiguous")
+    rows, heads, d = t.shape
+    return rows, heads, d, t.stride(0) if rows > 1 else heads * d
+
+
+def op_qk_norm_rope(q, k, q_gain, k_gain, rope, positions=None, pairing="adjacent", eps=1e-6, q_out=None, k_out=None,
+                    out_dtype=None, stream=None):
+    """RMSNorm of every head of q [rows, heads_q, d] and k [rows, heads_k, d] (BF16 or FP32; views of a
+    fused buffer pass as they lie; k may be None) and the rotation of its pairs by rope
+    [n_pos, rot_dim/2, 2] (cos, sin), or None for the norm alone.  Token r is at positions[r] (int32), or
+    r % n_pos.  Writes q_out and k_out (which may be q and k), or new tensors, BF16 unless out_dtype says
+    FP32.  Returns (q_out, k_out)."""
+    import torch
+    _on_current_device(q=q, k=k, q_gain=q_gain, k_gain=k_gain, rope=rope, positions=positions, q_out=q_out,
+                       k_out=k_out)
+    f = torch.float32
+    a = QkNormRopeArgs()
+    lib().moss_qk_norm_rope_args_init(ctypes.byref(a), ctypes.sizeof(QkNormRopeArgs))
+    a.in_dtype = _dtype_code(q, "q")
+    a.rows, a.heads_q, a.head_dim, a.q_stride = _heads_of(q, "q")
+    want = out_dtype or (q_out.dtype if q_out is not None else torch.bfloat16)
+    if q_out is None:
+        q_out = torch.empty(q.shape, device=q.device, dtype=want)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, device=k.device, dtype=want)
+    a.out_dtype = _dtype_code(q_out, "q_out")
+    for name, t, ref in (("q_out", q_out, q), ("k_out", k_out, k)):
+        if t is not None and (ref is None or t.shape != ref.shape or t.dtype != want):
+            raise MossError(1, f"{name} must have its input's shape and be {want}")
+    a.q_out_stride = _heads_of(q_out, "q_out")[3]
+    a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
+    d = a.head_dim
+    a.q_gain = _shaped(q_gain, (d,), f, "q_gain")
+    if k is not None:
+        rows, a.heads_k, dk, a.k_stride = _heads_of(k, "k")
+        if rows != a.rows or dk != d or k.dtype != q.dtype:
+            raise MossError(1, "k must have q's tokens, head_dim and type")
+        a.k_out_stride = _heads_of(k_out, "k_out")[3]
+        a.k, a.k_out = k.data_ptr(), k_out.data_ptr()
+        a.k_gain = _shaped(k_gain, (d,), f, "k_gain")
+    a.rot_dim = 0
+    if rope is not None:
+        if rope.dim() != 3 or rope.shape[2] != 2:
+            raise MossError(1, "rope must be [n_pos, rot_dim/2, 2]")
+        a.n_pos, a.rot_dim, a.rope = rope.shape[0], 2 * rope.shape[1], _ptr(rope, f, "rope")
+    a.positions = _shaped(positions, (a.rows,), torch.int32, "positions")
+    if pairing not in ROPE_PAIRINGS:
+        raise MossError(1, f"pairing must be one of {sorted(ROPE_PAIRINGS)}")
+    a.pairing = ROPE_PAIRINGS[pairing]
+    a.eps = eps
+    _check(lib().moss_op_qk_norm_rope(ctypes.byref(a), _stream(stream)))
+    return q_out, k_out
+
+
+def op_rope_table(grid_h: int, grid_w: int, n_txt: int, stream=None):
+    """The model's (cos, sin) for op_qk_norm_rope: CUDA FP32 [grid_h*grid_w + n_txt, 64, 2]."""
+    import torch
+    if grid_h < 0 or grid_w < 0 or n_txt < 0:
+        raise MossError(1, "grid_h, grid_w and n_txt must be >= 0")
+    table = torch.empty(grid_h * grid_w + n_txt, 64, 2, device="cuda", dtype=torch.float32)
+    _check(lib().moss_op_rope_table(table.data_ptr(), grid_h, grid_w, n_txt, _stream(stream)))
+    return table
 
 
 def _config_for(shape, layers: int) -> Config:

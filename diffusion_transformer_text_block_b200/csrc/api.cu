@@ -71,15 +71,28 @@ int num_sms() {
 static unsigned* g_err_word[64] = {nullptr};
 static std::mutex g_err_mu;
 
-static unsigned* device_error_word() {
+// Allocates and clears one error word.  The first call may come while a stream is being captured:
+// the allocation then needs the relaxed capture mode, and the clear a stream of its own (the legacy
+// stream would join the capture).
+static unsigned* new_error_word() {
+  unsigned* p = nullptr;
+  cudaStream_t s = nullptr;
+  bool ok = cudaMalloc(&p, 256) == cudaSuccess && cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) == cudaSuccess &&
+            cudaMemsetAsync(p, 0, 256, s) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess;
+  if (s) cudaStreamDestroy(s);
+  if (!ok && p) cudaFree(p);
+  return ok ? p : nullptr;
+}
+
+unsigned* device_error_word() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
   std::lock_guard<std::mutex> lk(g_err_mu);
   if (!g_err_word[dev]) {
-    unsigned* p = nullptr;
-    if (cudaMalloc(&p, 256) != cudaSuccess) return nullptr;
-    if (cudaMemset(p, 0, 256) != cudaSuccess) return nullptr;
-    g_err_word[dev] = p;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const bool swapped = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
+    g_err_word[dev] = new_error_word();
+    if (swapped) cudaThreadExchangeStreamCaptureMode(&mode);
   }
   return g_err_word[dev];
 }
@@ -120,6 +133,32 @@ bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint6
     if (err) {
       char buf[160];
       snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled failed (%d) for a [%llu, %llu] BF16 tensor", int(r),
+               (unsigned long long)outer, (unsigned long long)inner);
+      *err = buf;
+    }
+    return false;
+  }
+  return true;
+}
+
+bool make_tmap_i8_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
+                     uint32_t box_outer, std::string* err) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) {
+    if (err) *err = "cuTensorMapEncodeTiled is not available from the driver";
+    return false;
+  }
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {inner};
+  cuuint32_t box[2] = {box_inner, box_outer};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    if (err) {
+      char buf[160];
+      snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled failed (%d) for a [%llu, %llu] 8-bit tensor", int(r),
                (unsigned long long)outer, (unsigned long long)inner);
       *err = buf;
     }

@@ -288,14 +288,15 @@ __global__ void __launch_bounds__(256) mod_gemv_kernel(const bf16* __restrict__ 
 // (patch row), 40..63 (patch column), axis dims 32/48/48, theta 1e4; image token (r, c) at
 // (0, r, c), text token j at (j + 1, 0, 0).  Stored as (cos, sin) in FP32, computed in FP64,
 // pair-major: table[j * N + token], so that consecutive tokens (the rows a warp of the QKV
-// epilogue holds) read one contiguous segment.
-__global__ void rope_table_kernel(float2* __restrict__ table, int grid_h, int grid_w, int n_txt) {
+// epilogue holds) read one contiguous segment; or token-major, table[token * 64 + j], for a kernel
+// whose warp stays on one token.
+__global__ void rope_table_kernel(float2* __restrict__ table, int grid_h, int grid_w, int n_txt, bool pair_major) {
   const int n_img = grid_h * grid_w;
   const int n_tok = n_img + n_txt;
   const int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (e >= static_cast<int64_t>(n_tok) * 64) return;
-  const int j = static_cast<int>(e / n_tok);
-  const int tok = static_cast<int>(e % n_tok);
+  const int j = static_cast<int>(pair_major ? e / n_tok : e % 64);
+  const int tok = static_cast<int>(pair_major ? e % n_tok : e / 64);
   int p0 = 0, p1 = 0, p2 = 0;
   if (tok < n_img) {
     p1 = tok / grid_w;
@@ -430,10 +431,11 @@ cudaError_t launch_mod_gemv(const bf16* W, const bf16* bias, const float* sc, fl
   return cudaGetLastError();
 }
 
-cudaError_t launch_rope_table(float2* table, int grid_h, int grid_w, int n_txt, cudaStream_t s) {
+cudaError_t launch_rope_table(float2* table, int grid_h, int grid_w, int n_txt, cudaStream_t s, bool pair_major) {
   const int64_t n = static_cast<int64_t>(grid_h * grid_w + n_txt) * 64;
   if (n <= 0) return cudaSuccess;
-  rope_table_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(table, grid_h, grid_w, n_txt);
+  rope_table_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(table, grid_h, grid_w, n_txt,
+                                                                             pair_major);
   return cudaGetLastError();
 }
 

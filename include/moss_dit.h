@@ -329,7 +329,8 @@ int moss_sample_ex(moss_model* m, int steps, float cfg, double shift, uint64_t s
 /* Status, profiling and operator-level entry points (used by tests and the benchmark). */
 /* ------------------------------------------------------------------------------------ */
 
-/* Device error word set by a kernel whose bounded wait gave up (0 = none).  Synchronises
+/* Device error word set by a kernel whose bounded wait gave up, or that met a token position outside
+ * its angle table (moss_op_qk_norm_rope, 0x401); 0 = none.  Synchronises
  * the device.  clear != 0 resets it.  Returns the word (>= 0) or -MOSS_ERR_CUDA. */
 int moss_device_status(int clear);
 
@@ -396,6 +397,110 @@ int moss_op_ln_modulate(const float* x, const float* shift, const float* scale, 
 /* Timestep conditioning of the model at time t: writes the modulation vectors of all
  * layers and of the final layer, mod device FP32 [L*6D + 2D]. */
 int moss_op_modulation(moss_model* m, float t, float* mod, void* stream);
+
+/* ------------------------------------------------------------------------------------ */
+/* The 8-bit linear path: a block's linear layers on 8-bit integers (an opt-in, lossy     */
+/* alternative to the BF16 products; [INV] Transformer formats and [MI] What works name   */
+/* 8-bit integer forms of the linear layers).  Rows of activations get one scale each,    */
+/* output channels of the weights one scale each; sums are exact 32-bit integers.         */
+/*                                                                                        */
+/* One joint block from these calls: ln_modulate_i8, gemm_i8 (q|k|v, BF16),               */
+/* qk_norm_rope in place, moss_op_attention, quantize_i8, gemm_i8 into the residual       */
+/* stream, ln_modulate_i8, gemm_i8 (gate|up, BF16), swiglu_i8, gemm_i8 into the stream.   */
+/* Inference only, like the rest of the library: there are no backward passes.            */
+/* Calls take buffers of the current device; rows == 0 (M == 0) launches nothing.         */
+/* ------------------------------------------------------------------------------------ */
+enum { MOSS_DTYPE_F32 = 0, MOSS_DTYPE_BF16 = 1 };
+
+/* Rows to 8-bit integers: amax = max_j |x[r,j]|, scale[r] = amax / 127 (FP32), q[r,j] = the integer
+ * nearest to 127 x[r,j] / amax, halves to even: -127..127, exactly so for every finite row.  A row of
+ * zeros has scale 0 and q 0; a row with an infinity or a NaN has scale NaN and q 0.
+ *   x:      device [rows, dim] of x_dtype (MOSS_DTYPE_*), x_stride elements between rows
+ *           (>= dim, a multiple of 16 bytes), 16-byte aligned
+ *   q:      device int8 [rows, dim], 16-byte aligned;  scale: device FP32 [rows]
+ * dim: a multiple of 16, at most 32768.  The outputs must not overlap the input.
+ * moss_op_gemm_i8 takes (q, scale) as A, and the same made of a weight [N, K] as B.
+ * Errors: INVALID_ARGUMENT (the above; a NULL or misaligned pointer; rows < 0), CUDA. */
+int moss_op_quantize_i8(const void* x, int x_dtype, int64_t x_stride, int8_t* q, float* scale, int rows, int dim,
+                        void* stream);
+
+/* moss_op_ln_modulate with its rows made 8-bit: h = LN(x)(1 + scale) + shift in FP32 (eps 1e-6, biased
+ * variance), not rounded in between, then q and q_scale from h as in moss_op_quantize_i8.
+ *   x: device FP32 [rows, dim]; shift, scale: device FP32 [dim]; q: device int8 [rows, dim];
+ *   all 16-byte aligned; q_scale: device FP32 [rows].  dim as for moss_op_quantize_i8.
+ * Errors: as moss_op_quantize_i8. */
+int moss_op_ln_modulate_i8(const float* x, const float* shift, const float* scale, int8_t* q, float* q_scale, int rows,
+                           int dim, void* stream);
+
+/* The feed-forward activation made 8-bit: h = SiLU(g) * u in FP32, not rounded in between, then q and
+ * scale from h as in moss_op_quantize_i8.
+ *   gu: device BF16 [rows, 2 dim], each row g | u, gu_stride elements between rows (>= 2 dim, a
+ *       multiple of 8), 16-byte aligned;  q: device int8 [rows, dim], 16-byte aligned;
+ *   scale: device FP32 [rows].  dim as for moss_op_quantize_i8.
+ * Errors: as moss_op_quantize_i8. */
+int moss_op_swiglu_i8(const void* gu, int64_t gu_stride, int8_t* q, float* scale, int rows, int dim, void* stream);
+
+/* 8-bit GEMM: with v = (sum_k a[m,k] b[n,k]) a_scale[m] b_scale[n] + bias[n],
+ *   c[m,n] = v,  or with gate and residual  c[m,n] = residual[m,n] + gate[n] v.
+ *   a: device int8 [M, K];  a_scale: device FP32 [M];  b: device int8 [N, K];  b_scale: device FP32 [N]
+ *   bias: device BF16 [N] or NULL;  gate: device FP32 [N] and residual: device FP32 [M, N], both or
+ *   neither (FP32 c only); residual may be c itself (the update in place)
+ *   c: device [M, N] of c_dtype.  a, b, c and residual 16-byte aligned.
+ * M >= 0 and N >= 1 of any size, K a multiple of 16 up to 65536 (the sums then fit 32 bits).  The sums
+ * are exact; a sum is rounded to FP32 once, scales, bias, gate and residual are applied in FP32, and a
+ * BF16 c is rounded once at the end.  c does not depend on how the work is split.
+ * Errors: INVALID_ARGUMENT (the above, or c overlaps an input), CUDA.  A device-side wait that gives up
+ * after 2 s sets the device error word (0x111 producer, 0x112 MMA, 0x113 epilogue). */
+int moss_op_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale, const void* bias,
+                    const float* gate, const float* residual, void* c, int c_dtype, int M, int N, int K, void* stream);
+
+/* ------------------------------------------------------------------------------------ */
+/* Query/key norm and rotation: what moss_op_attention expects done to q and k.           */
+/* ------------------------------------------------------------------------------------ */
+enum { MOSS_ROPE_ADJACENT = 0, MOSS_ROPE_HALVES = 1 };
+
+/* q and k of `rows` tokens: heads_q (heads_k) heads of head_dim elements, one after the other, the
+ * tokens q_stride (k_stride) elements apart, so the parts of a fused q|k|v buffer pass as they lie. */
+typedef struct moss_qk_norm_rope_args {
+  uint32_t struct_size;    /* sizeof(moss_qk_norm_rope_args) as compiled by the caller              */
+  int32_t in_dtype;        /* MOSS_DTYPE_* of q and k                                               */
+  int32_t out_dtype;       /* MOSS_DTYPE_* of q_out and k_out                                       */
+  int32_t rows;            /* tokens                                                                */
+  int32_t heads_q;         /* >= 1                                                                  */
+  int32_t heads_k;         /* >= 0; 0: no keys, the k fields are ignored                            */
+  int32_t head_dim;        /* 64, 128 or 256                                                        */
+  int32_t rot_dim;         /* leading elements of a head that are rotated: a multiple of 8, at most
+                              head_dim; 0: none (rope, positions and n_pos are then unused)         */
+  int32_t pairing;         /* MOSS_ROPE_ADJACENT: pair i = elements (2i, 2i+1), the model's own;
+                              MOSS_ROPE_HALVES: pair i = (i, i + rot_dim/2)                         */
+  int32_t n_pos;           /* positions in rope                                                     */
+  float eps;               /* of the RMSNorm                                                        */
+  int32_t reserved;        /* 0                                                                     */
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;  /* elements between tokens; multiples of 16 bytes */
+  const void* q;           /* device, 16-byte aligned (as all pointers here but positions)          */
+  const void* k;
+  void* q_out;             /* its own input (same address, stride and type), or disjoint from all   */
+  void* k_out;
+  const float* q_gain;     /* device FP32 [head_dim], or NULL for 1                                 */
+  const float* k_gain;
+  const float* rope;       /* device FP32 [n_pos, rot_dim/2, 2]: (cos, sin) of each pair            */
+  const int32_t* positions;/* device [rows], each in [0, n_pos); or NULL: token r is at r % n_pos   */
+} moss_qk_norm_rope_args;
+
+/* BF16 in and out, head_dim = rot_dim = 128, adjacent pairs, eps 1e-6, the rest 0; struct_size as given. */
+void moss_qk_norm_rope_args_init(moss_qk_norm_rope_args* args, uint32_t struct_size);
+
+/* y = x * rsqrt(mean(x^2) + eps) * gain over each head, then each pair (a, b) of the first rot_dim
+ * elements becomes (a cos - b sin, a sin + b cos); in FP32, rounded once at the end.  A NaN makes its
+ * whole head NaN, an infinity its pair NaN and the rest of its head 0.  A token whose position is outside [0, n_pos) is left out
+ * (its output is not written) and sets the device error word to 0x401.
+ * Errors: ABI_MISMATCH (struct_size), UNSUPPORTED (head_dim), INVALID_ARGUMENT (the rules above), CUDA. */
+int moss_op_qk_norm_rope(const moss_qk_norm_rope_args* args, void* stream);
+
+/* The model's angles as moss_op_qk_norm_rope takes them (head_dim 128, adjacent pairs): table device
+ * FP32 [grid_h*grid_w + n_txt, 64, 2], token order [image row-major; text] as in the residual stream,
+ * 16-byte aligned.  Errors: INVALID_ARGUMENT (a negative size, over 2^24 tokens, NULL or misaligned). */
+int moss_op_rope_table(float* table, int grid_h, int grid_w, int n_txt, void* stream);
 
 /* ------------------------------------------------------------------------------------ */
 /* Allocation-free entry point.                                                          */
