@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -267,24 +268,54 @@ def op_ln_modulate(x, shift, scale, stream=None):
 
 
 # ----------------------------------------------------------------------------- the 8-bit linear path
-def _on_current_device(**tensors):
-    """The library launches on the current device: refuse tensors of another one (or of the host)."""
-    import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for name, t in tensors.items():
-        if t is None:
-            continue
+# A call on a few tokens takes a few microseconds on the GPU, so these wrappers keep the host's part short:
+# one pass over each argument, no device queries beyond the current device and its stream.
+_torch = None
+
+
+def _begin(t, name):
+    """(torch, current device) for a call whose first argument is t."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    if not t.is_cuda:
+        raise MossError(1, f"{name} must be a CUDA tensor")
+    return _torch, _torch._C._cuda_getDevice()
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
+
+
+def _placed(t, dev, dtype, name):
+    """Refuse a tensor that is not of this type (None: any) on the current device: the library launches there."""
+    if t.get_device() != dev:
         if not t.is_cuda:
             raise MossError(1, f"{name} must be a CUDA tensor")
-        if t.device.index != dev:
-            raise MossError(1, f"{name} is on cuda:{t.device.index}, not on the current device cuda:{dev}")
+        raise MossError(1, f"{name} is on cuda:{t.get_device()}, not on the current device cuda:{dev}")
+    if dtype is not None and t.dtype is not dtype:
+        raise MossError(1, f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _arg(t, dev, dtype, shape, name):
+    """Address of a contiguous tensor of this type and shape on the current device; None stays None."""
+    if t is None:
+        return None
+    _placed(t, dev, dtype, name)
+    if t.shape != shape:
+        raise MossError(1, f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise MossError(1, f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _dtype_code(t, name):
-    import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is _torch.bfloat16:
         return DTYPE_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is _torch.float32:
         return DTYPE_F32
     raise MossError(1, f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
 
@@ -293,58 +324,50 @@ def _rows_of(t, name):
     """(rows, width, stride between rows) of a 2-D tensor whose rows are contiguous."""
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise MossError(1, f"{name} must be [rows, dim] with contiguous rows")
-    return t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _shaped(t, shape, dtype, name):
-    """A contiguous tensor of this shape and type, as a pointer (None stays None)."""
-    if t is not None and tuple(t.shape) != shape:
-        raise MossError(1, f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return _ptr(t, dtype, name)
+    rows, width = t.shape
+    return rows, width, t.stride(0) if rows > 1 else width
 
 
 def op_quantize_i8(x, stream=None):
     """Rows of x [rows, dim] (BF16 or FP32; rows may lie apart) to (q int8 [rows, dim], scale FP32
     [rows]): q = round(127 x / amax), halves to even, scale = amax / 127."""
-    import torch
-    _on_current_device(x=x)
+    torch, dev = _begin(x, "x")
+    _placed(x, dev, None, "x")
     code = _dtype_code(x, "x")
     rows, dim, stride = _rows_of(x, "x")
-    q = torch.empty(rows, dim, device=x.device, dtype=torch.int8)
-    scale = torch.empty(rows, device=x.device, dtype=torch.float32)
+    q = x.new_empty((rows, dim), dtype=torch.int8)
+    scale = x.new_empty(rows, dtype=torch.float32)
     _check(lib().moss_op_quantize_i8(x.data_ptr(), code, stride, q.data_ptr(), scale.data_ptr(), rows, dim,
-                                     _stream(stream)))
+                                     _raw_stream(stream, dev)))
     return q, scale
 
 
 def op_ln_modulate_i8(x, shift, scale, stream=None):
     """LN(x) (1 + scale) + shift of FP32 x [rows, dim], made 8-bit by rows: (q int8, q_scale FP32 [rows])."""
-    import torch
-    _on_current_device(x=x, shift=shift, scale=scale)
+    torch, dev = _begin(x, "x")
     rows, dim = x.shape
     f = torch.float32
-    q = torch.empty(rows, dim, device=x.device, dtype=torch.int8)
-    q_scale = torch.empty(rows, device=x.device, dtype=f)
-    _check(lib().moss_op_ln_modulate_i8(_ptr(x, f, "x"), _shaped(shift, (dim,), f, "shift"),
-                                        _shaped(scale, (dim,), f, "scale"), q.data_ptr(), q_scale.data_ptr(), rows,
-                                        dim, _stream(stream)))
+    q = x.new_empty((rows, dim), dtype=torch.int8)
+    q_scale = x.new_empty(rows)
+    _check(lib().moss_op_ln_modulate_i8(_arg(x, dev, f, x.shape, "x"), _arg(shift, dev, f, (dim,), "shift"),
+                                        _arg(scale, dev, f, (dim,), "scale"), q.data_ptr(), q_scale.data_ptr(), rows,
+                                        dim, _raw_stream(stream, dev)))
     return q, q_scale
 
 
 def op_swiglu_i8(gu, stream=None):
     """SiLU(g) * u of BF16 gu [rows, 2 dim] (each row g | u; rows may lie apart), made 8-bit by rows:
     (q int8 [rows, dim], scale FP32 [rows])."""
-    import torch
-    _on_current_device(gu=gu)
-    if gu.dtype != torch.bfloat16:
-        raise MossError(1, f"gu must be torch.bfloat16, got {gu.dtype}")
+    torch, dev = _begin(gu, "gu")
+    _placed(gu, dev, torch.bfloat16, "gu")
     rows, width, stride = _rows_of(gu, "gu")
     if width % 2:
         raise MossError(1, "gu must hold gate and up halves of one width")
-    q = torch.empty(rows, width // 2, device=gu.device, dtype=torch.int8)
-    scale = torch.empty(rows, device=gu.device, dtype=torch.float32)
-    _check(lib().moss_op_swiglu_i8(gu.data_ptr(), stride, q.data_ptr(), scale.data_ptr(), rows, width // 2,
-                                   _stream(stream)))
+    dim = width // 2
+    q = gu.new_empty((rows, dim), dtype=torch.int8)
+    scale = gu.new_empty(rows, dtype=torch.float32)
+    _check(lib().moss_op_swiglu_i8(gu.data_ptr(), stride, q.data_ptr(), scale.data_ptr(), rows, dim,
+                                   _raw_stream(stream, dev)))
     return q, scale
 
 
@@ -352,32 +375,46 @@ def op_gemm_i8(a, a_scale, b, b_scale, bias=None, gate=None, residual=None, out_
     """(A B^T) a_scale[:, None] b_scale + bias of int8 A [M, K] and B [N, K], BF16 unless out_dtype or out
     says FP32; with gate [N] and residual [M, N] (FP32): residual + gate * that, in FP32.  out may be the
     residual."""
-    import torch
-    _on_current_device(a=a, a_scale=a_scale, b=b, b_scale=b_scale, bias=bias, gate=gate, residual=residual, out=out)
+    torch, dev = _begin(a, "a")
     if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
         raise MossError(1, "a must be [M, K] and b [N, K]")
     M, K = a.shape
     N = b.shape[0]
-    f = torch.float32
+    f, i8 = torch.float32, torch.int8
     if out is None:
-        out = torch.empty(M, N, device=a.device,
-                          dtype=out_dtype or (f if residual is not None else torch.bfloat16))
-    elif out_dtype is not None and out.dtype != out_dtype:
+        out = a.new_empty((M, N), dtype=out_dtype or (f if residual is not None else torch.bfloat16))
+    elif out_dtype is not None and out.dtype is not out_dtype:
         raise MossError(1, f"out is {out.dtype}, not {out_dtype}")
     _check(lib().moss_op_gemm_i8(
-        _ptr(a, torch.int8, "a"), _shaped(a_scale, (M,), f, "a_scale"), _ptr(b, torch.int8, "b"),
-        _shaped(b_scale, (N,), f, "b_scale"), _shaped(bias, (N,), torch.bfloat16, "bias"),
-        _shaped(gate, (N,), f, "gate"), _shaped(residual, (M, N), f, "residual"), _shaped(out, (M, N), None, "out"),
-        _dtype_code(out, "out"), M, N, K, _stream(stream)))
+        _arg(a, dev, i8, (M, K), "a"), _arg(a_scale, dev, f, (M,), "a_scale"), _arg(b, dev, i8, (N, K), "b"),
+        _arg(b_scale, dev, f, (N,), "b_scale"), _arg(bias, dev, torch.bfloat16, (N,), "bias"),
+        _arg(gate, dev, f, (N,), "gate"), _arg(residual, dev, f, (M, N), "residual"),
+        _arg(out, dev, None, (M, N), "out"), _dtype_code(out, "out"), M, N, K, _raw_stream(stream, dev)))
     return out
 
 
-def _heads_of(t, name):
-    """(rows, heads, head_dim, stride between tokens) of [rows, heads, head_dim] with packed heads."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+def _heads_of(t, dev, name):
+    """(shape, stride between tokens, address) of [tokens, heads, head_dim] whose heads are packed."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
         raise MossError(1, f"{name} must be [tokens, heads, head_dim] with each token's heads contiguous")
-    rows, heads, d = t.shape
-    return rows, heads, d, t.stride(0) if rows > 1 else heads * d
+    if t.get_device() != dev:
+        _placed(t, dev, None, name)
+    return shape, stride[0] if shape[0] > 1 else shape[1] * shape[2], t.data_ptr()
+
+
+def _heads_out(t, ref, shape, dtype, dev, name):
+    """(tensor, stride between tokens, address) of an output of ref's shape: t, or a new one."""
+    if t is None:
+        t = ref.new_empty(shape, dtype=dtype)
+        return t, shape[1] * shape[2], t.data_ptr()
+    out_shape, stride, ptr = _heads_of(t, dev, name)
+    if out_shape != shape or t.dtype is not dtype:
+        raise MossError(1, f"{name} must have its input's shape and be {dtype}")
+    return t, stride, ptr
+
+
+_pack_qk = struct.Struct("@I9ifi4q8Q").pack  # QkNormRopeArgs' fields in order
 
 
 def op_qk_norm_rope(q, k, q_gain, k_gain, rope, positions=None, pairing="adjacent", eps=1e-6, q_out=None, k_out=None,
@@ -387,45 +424,36 @@ def op_qk_norm_rope(q, k, q_gain, k_gain, rope, positions=None, pairing="adjacen
     [n_pos, rot_dim/2, 2] (cos, sin), or None for the norm alone.  Token r is at positions[r] (int32), or
     r % n_pos.  Writes q_out and k_out (which may be q and k), or new tensors, BF16 unless out_dtype says
     FP32.  Returns (q_out, k_out)."""
-    import torch
-    _on_current_device(q=q, k=k, q_gain=q_gain, k_gain=k_gain, rope=rope, positions=positions, q_out=q_out,
-                       k_out=k_out)
+    torch, dev = _begin(q, "q")
     f = torch.float32
-    a = QkNormRopeArgs()
-    lib().moss_qk_norm_rope_args_init(ctypes.byref(a), ctypes.sizeof(QkNormRopeArgs))
-    a.in_dtype = _dtype_code(q, "q")
-    a.rows, a.heads_q, a.head_dim, a.q_stride = _heads_of(q, "q")
-    want = out_dtype or (q_out.dtype if q_out is not None else torch.bfloat16)
-    if q_out is None:
-        q_out = torch.empty(q.shape, device=q.device, dtype=want)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, device=k.device, dtype=want)
-    a.out_dtype = _dtype_code(q_out, "q_out")
-    for name, t, ref in (("q_out", q_out, q), ("k_out", k_out, k)):
-        if t is not None and (ref is None or t.shape != ref.shape or t.dtype != want):
-            raise MossError(1, f"{name} must have its input's shape and be {want}")
-    a.q_out_stride = _heads_of(q_out, "q_out")[3]
-    a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
-    d = a.head_dim
-    a.q_gain = _shaped(q_gain, (d,), f, "q_gain")
-    if k is not None:
-        rows, a.heads_k, dk, a.k_stride = _heads_of(k, "k")
-        if rows != a.rows or dk != d or k.dtype != q.dtype:
-            raise MossError(1, "k must have q's tokens, head_dim and type")
-        a.k_out_stride = _heads_of(k_out, "k_out")[3]
-        a.k, a.k_out = k.data_ptr(), k_out.data_ptr()
-        a.k_gain = _shaped(k_gain, (d,), f, "k_gain")
-    a.rot_dim = 0
-    if rope is not None:
-        if rope.dim() != 3 or rope.shape[2] != 2:
-            raise MossError(1, "rope must be [n_pos, rot_dim/2, 2]")
-        a.n_pos, a.rot_dim, a.rope = rope.shape[0], 2 * rope.shape[1], _ptr(rope, f, "rope")
-    a.positions = _shaped(positions, (a.rows,), torch.int32, "positions")
     if pairing not in ROPE_PAIRINGS:
         raise MossError(1, f"pairing must be one of {sorted(ROPE_PAIRINGS)}")
-    a.pairing = ROPE_PAIRINGS[pairing]
-    a.eps = eps
-    _check(lib().moss_op_qk_norm_rope(ctypes.byref(a), _stream(stream)))
+    shape, q_stride, q_ptr = _heads_of(q, dev, "q")
+    rows, heads_q, d = shape
+    want = out_dtype or (q_out.dtype if q_out is not None else torch.bfloat16)
+    q_out, qo_stride, qo_ptr = _heads_out(q_out, q, shape, want, dev, "q_out")
+    heads_k, k_stride, ko_stride, k_ptr, ko_ptr = 0, 0, 0, 0, 0
+    if k is not None:
+        shape, k_stride, k_ptr = _heads_of(k, dev, "k")
+        heads_k = shape[1]
+        if shape[0] != rows or shape[2] != d or k.dtype is not q.dtype:
+            raise MossError(1, "k must have q's tokens, head_dim and type")
+        k_out, ko_stride, ko_ptr = _heads_out(k_out, k, shape, want, dev, "k_out")
+    elif k_out is not None or k_gain is not None:
+        raise MossError(1, "k_out and k_gain go with k")
+    n_pos, rot_dim, rope_ptr = 0, 0, None
+    if rope is not None:
+        shape = rope.shape
+        if len(shape) != 3 or shape[2] != 2:
+            raise MossError(1, "rope must be [n_pos, rot_dim/2, 2]")
+        rope_ptr = _arg(rope, dev, f, shape, "rope")
+        n_pos, rot_dim = shape[0], 2 * shape[1]
+    a = QkNormRopeArgs.from_buffer_copy(_pack_qk(
+        ctypes.sizeof(QkNormRopeArgs), _dtype_code(q, "q"), _dtype_code(q_out, "q_out"), rows, heads_q, heads_k, d,
+        rot_dim, ROPE_PAIRINGS[pairing], n_pos, eps, 0, q_stride, k_stride, qo_stride, ko_stride, q_ptr, k_ptr, qo_ptr,
+        ko_ptr, _arg(q_gain, dev, f, (d,), "q_gain") or 0, _arg(k_gain, dev, f, (d,), "k_gain") or 0, rope_ptr or 0,
+        _arg(positions, dev, torch.int32, (rows,), "positions") or 0))
+    _check(lib().moss_op_qk_norm_rope(ctypes.byref(a), _raw_stream(stream, dev)))
     return q_out, k_out
 
 

@@ -154,3 +154,11 @@ def test_binding_refuses_host_tensors():
                  lambda: moss.op_qk_norm_rope(x.view(4, 1, 64), None, None, None, None)):
         with pytest.raises(moss.MossError, match="must be a CUDA tensor"):
             call()
+
+
+def test_the_packed_arguments_are_the_structure():
+    """The binding packs the query/key arguments in one go: field for field what the structure declares."""
+    n = len(moss.QkNormRopeArgs._fields_)
+    values = [float(i) if name == "eps" else i + 1 for i, (name, _) in enumerate(moss.QkNormRopeArgs._fields_)]
+    a = moss.QkNormRopeArgs.from_buffer_copy(moss._pack_qk(*values))
+    assert [getattr(a, name) for name, _ in moss.QkNormRopeArgs._fields_] == values and n == 24
