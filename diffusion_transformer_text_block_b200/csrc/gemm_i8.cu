@@ -34,18 +34,17 @@ struct FlatShape {
   static constexpr int kWBytes = kTileN * kBK;
   static constexpr int kXBytes = NT * kBK;
   static constexpr int kStageBytes = kWBytes + kXBytes;
-  static constexpr int kStages = (208 * 1024) / kStageBytes < 8 ? (208 * 1024) / kStageBytes : 8;
-  static constexpr int kPartBytes = kTileN * NT * 4;  // partial sums of a tile, in the slots' place
+  static constexpr int kPartBytes = kTileN * NT * 4;  // partial sums a CTA receives from its cluster
+  // Two CTAs a SM up to 64 tokens, one above.
+  static constexpr int kCtas = NT <= 64 ? 2 : 1;
+  static constexpr int kStages = ((kCtas == 2 ? 111 : 224) * 1024 - kPartBytes) / kStageBytes;
   static constexpr int kTmemCols = NT < 32 ? 32 : NT;
-  static constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 256;
-  static_assert(kPartBytes <= kStages * kStageBytes, "partial sums fit the slots");
-  static_assert(kStageBytes % 1024 == 0 && kSmemBytes <= 227 * 1024, "shared memory");
+  static constexpr int kSmemBytes = kStages * kStageBytes + kPartBytes + NT * 4 + 1024 + 256;
+  static_assert(kStages >= 3 && kStageBytes % 1024 == 0 && kCtas * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // Let the loads already issued land (bounded as well): after an abort too, no copy is in flight when
@@ -66,8 +65,9 @@ __device__ __forceinline__ void drain_loads(uint64_t* full, const int (&armed)[S
 struct I8Channel {
   float scale, bias, gate;
 };
-__device__ __forceinline__ void store_value(const GemmI8Params& p, const I8Channel& ch, int acc, int m, int n) {
-  float v = fmaf(__int2float_rn(acc) * __ldg(p.a_scale + m), ch.scale, ch.bias);
+__device__ __forceinline__ void store_value(const GemmI8Params& p, const I8Channel& ch, int acc, float a_scale, int m,
+                                            int n) {
+  float v = fmaf(__int2float_rn(acc) * a_scale, ch.scale, ch.bias);
   const int64_t at = static_cast<int64_t>(m) * p.N + n;
   if (p.residual) v = fmaf(ch.gate, v, p.residual[at]);
   if (p.c_bf16)
@@ -77,7 +77,7 @@ __device__ __forceinline__ void store_value(const GemmI8Params& p, const I8Chann
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kFlatThreads, 1)
+__global__ void __launch_bounds__(kFlatThreads, FlatShape<NT>::kCtas)
     gemm_i8_flat_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                         const GemmI8Params p, int split, unsigned* err) {
   using S = FlatShape<NT>;
@@ -85,7 +85,9 @@ __global__ void __launch_bounds__(kFlatThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sW = smem;
   uint8_t* sX = smem + S::kStages * S::kWBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kStages * S::kStageBytes);
+  uint32_t* part = reinterpret_cast<uint32_t*>(smem + S::kStages * S::kStageBytes);
+  float* scales = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes + S::kPartBytes);  // of the tile's tokens
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + NT);
   uint64_t* empty = full + S::kStages;
   uint64_t* tfull = empty + S::kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
@@ -123,6 +125,7 @@ __global__ void __launch_bounds__(kFlatThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  if (split > 1) cluster_arrive();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -186,6 +189,8 @@ __global__ void __launch_bounds__(kFlatThreads, 1)
       if (p.bias) ch.bias = __bfloat162float(p.bias[n]);
       if (p.gate) ch.gate = __ldg(p.gate + n);
     }
+    for (int i = ln; i < NT; i += 128) scales[i] = m0 + i < p.M ? __ldg(p.a_scale + m0 + i) : 0.f;
+    asm volatile("bar.sync 1, 128;" ::: "memory");  // the four epilogue warps
     ok = mbar_wait(tfull, 0, err, kErrGemmI8Epilogue, abort_flag) && !*abort_flag;
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
@@ -199,37 +204,41 @@ __global__ void __launch_bounds__(kFlatThreads, 1)
         if (n < p.N) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (m0 + c + i < p.M) store_value(p, ch, static_cast<int>(v[i]), m0 + c + i, n);
+            if (m0 + c + i < p.M) store_value(p, ch, static_cast<int>(v[i]), scales[c + i], m0 + c + i, n);
         }
       }
     }
   } else {
-    // Every CTA of the cluster lays its partial sums out as [token][channel], then finishes its
-    // share of the tokens.  The slots are free: all loads of this CTA fed MMAs that have completed.
-    uint32_t* part = reinterpret_cast<uint32_t*>(smem);
+    // split is a power of two: CTA r finishes the tile's tokens [r share, (r + 1) share), and every CTA
+    // writes its partial sums of them to r's shared memory, [CTA][token][channel].
+    const int shift = __popc(NT / split - 1), share = 1 << shift;
     const int tokens = min(NT, p.M - m0);
+    __syncwarp();
+    cluster_wait();  // every CTA of the cluster has started
     if (epi && ok) {
+      const uint32_t mine = smem_u32(part + rank * share * kTileN + ln);
 #pragma unroll 1
       for (int c = 0; c < tokens; c += 16) {
         uint32_t v[16];
         tmem_ld16(tb + c, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) part[(c + i) * kTileN + ln] = v[i];
+        for (int i = 0; i < 16; ++i)
+          if (c + i < tokens)
+            st_cluster_u32(mapa_shared(mine + ((c + i) & (share - 1)) * kTileN * 4, (c + i) >> shift), v[i]);
       }
     }
     __syncwarp();
     cluster_sync();
     if (epi && ok && n < p.N) {
-      const int c0 = tokens * rank / split, c1 = tokens * (rank + 1) / split;
-      for (int c = c0; c < c1; ++c) {
-        const uint32_t at = smem_u32(part + c * kTileN + ln);
+      const int c0 = rank * share, count = min(share, tokens - c0);
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) {
         uint32_t sum = 0;
-        for (int r = 0; r < split; ++r) sum += ld_cluster_u32(mapa_shared(at, r));
-        store_value(p, ch, static_cast<int>(sum), m0 + c, n);
+#pragma unroll 4
+        for (int r = 0; r < split; ++r) sum += part[(r * share + i) * kTileN + ln];
+        store_value(p, ch, static_cast<int>(sum), scales[c0 + i], m0 + c0 + i, n);
       }
     }
-    __syncwarp();
-    cluster_sync();  // the peers have read this CTA's shared memory
   }
 
   tc_fence_before();
@@ -269,13 +278,122 @@ cudaError_t launch_flat(const int8_t* a, const int8_t* b, const GemmI8Params& p,
   return cudaLaunchKernelEx(&cfg, gemm_i8_flat_kernel<NT>, tw, tx, p, split, err);
 }
 
+cudaError_t launch_flat_nt(int nt, const int8_t* a, const int8_t* b, const GemmI8Params& p, int split, cudaStream_t s,
+                           unsigned* err, std::string* emsg) {
+  switch (nt) {
+    case 16: return launch_flat<16>(a, b, p, split, s, err, emsg);
+    case 32: return launch_flat<32>(a, b, p, split, s, err, emsg);
+    case 64: return launch_flat<64>(a, b, p, split, s, err, emsg);
+    default: return launch_flat<128>(a, b, p, split, s, err, emsg);
+  }
+}
+
+// ------------------------------------------------------------------------ a few tokens
+constexpr int kDotThreads = 256;
+constexpr int kDotWarps = kDotThreads / 32;
+
+// 16 bytes of weights, read once: past L1.
+__device__ __forceinline__ int4 ld_weights(const int4* p) {
+  int4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int dot16(const int4& a, const int4& b, int c) {
+  return __dp4a(a.w, b.w, __dp4a(a.z, b.z, __dp4a(a.y, b.y, __dp4a(a.x, b.x, c))));
+}
+
+// wk warps of a block (a power of two) share R channels: each takes the 512-byte pieces wk apart.
+template <int MT, int R, int U>
+__global__ void __launch_bounds__(kDotThreads) gemm_i8_dot_kernel(const int8_t* __restrict__ a,
+                                                                   const int8_t* __restrict__ b, const GemmI8Params p,
+                                                                   int wk) {
+  __shared__ int part[kDotWarps][R * MT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / wk, sub = warp & (wk - 1);
+  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * (kDotWarps / wk) + group) * R;
+  const int chunks = p.K >> 4;  // 16-byte pieces of a row
+  const int4* w[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    w[r] = reinterpret_cast<const int4*>(b + (n0 + r < p.N ? n0 + r : p.N - 1) * p.K);
+  int acc[R][MT];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[r][t] = 0;
+  const int4 zero = make_int4(0, 0, 0, 0);
+  for (int c0 = sub * 32 + lane; c0 - lane < chunks; c0 += U * wk * 32) {
+    int4 wv[U][R];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int c = c0 + u * wk * 32;
+        wv[u][r] = c < chunks ? ld_weights(w[r] + c) : zero;
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * wk * 32;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const int4 x = c < chunks && t < p.M ? __ldg(reinterpret_cast<const int4*>(a + static_cast<int64_t>(t) * p.K) + c) : zero;
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r][t] = dot16(wv[u][r], x, acc[r][t]);
+      }
+    }
+  }
+  // Lane r * MT + t ends with the sum of channel r and token t.
+  int mine = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int sum = __reduce_add_sync(0xffffffffu, acc[r][t]);
+      if (lane == r * MT + t) mine = sum;
+    }
+  if (wk > 1) {
+    if (lane < R * MT) part[warp][lane] = mine;
+    __syncthreads();
+    if (sub != 0) return;
+    mine = 0;
+    if (lane < R * MT)
+      for (int k = 0; k < wk; ++k) mine += part[warp + k][lane];
+  }
+  const int64_t n = n0 + lane / MT;
+  const int t = lane % MT;
+  if (lane >= R * MT || n >= p.N || t >= p.M) return;
+  I8Channel ch = {__ldg(p.b_scale + n), 0.f, 0.f};
+  if (p.bias) ch.bias = __bfloat162float(p.bias[n]);
+  if (p.gate) ch.gate = __ldg(p.gate + n);
+  store_value(p, ch, mine, __ldg(p.a_scale + t), t, static_cast<int>(n));
+}
+
+template <int MT, int R, int U>
+cudaError_t launch_dot_mt(const int8_t* a, const int8_t* b, const GemmI8Params& p, cudaStream_t s) {
+  const int64_t groups = (static_cast<int64_t>(p.N) + R - 1) / R;
+  // Warps per group of channels: until every SM has two blocks, while each warp keeps a piece of K.
+  int wk = 1;
+  while (wk < kDotWarps && groups * wk < static_cast<int64_t>(num_sms()) * 2 * kDotWarps && p.K > 512 * wk) wk *= 2;
+  const unsigned grid = static_cast<unsigned>((groups * wk + kDotWarps - 1) / kDotWarps);
+  gemm_i8_dot_kernel<MT, R, U><<<grid, kDotThreads, 0, s>>>(a, b, p, wk);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dot(const int8_t* a, const int8_t* b, const GemmI8Params& p, cudaStream_t s) {
+  if (p.M == 1) return launch_dot_mt<1, 4, 2>(a, b, p, s);
+  if (p.M == 2) return launch_dot_mt<2, 4, 2>(a, b, p, s);
+  if (p.M <= 4) return launch_dot_mt<4, 4, 2>(a, b, p, s);
+  return launch_dot_mt<8, 4, 2>(a, b, p, s);
+}
+
 // ------------------------------------------------------------------------ CTA pairs
 constexpr int kPairThreads = 320;    // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
 constexpr int kPairStages = 6;
 constexpr int kPairOpBytes = 128 * kBK;                 // one operand's rows of one CTA in a slot
 constexpr int kPairStageBytes = 2 * kPairOpBytes;       // 32 KB
-constexpr int kPairColBytes = 8 * 3 * 128 * 4;          // per epilogue warp: scale, bias, gate of its 128 columns
-constexpr int kPairSmemBytes = kPairStages * kPairStageBytes + kPairColBytes + 1024 + 256;
+constexpr int kPairSmemBytes = kPairStages * kPairStageBytes + 1024 + 256;
 static_assert(kPairSmemBytes <= 227 * 1024, "shared memory");
 constexpr int kPairGroupM = 16;      // M-tiles per band of the tile order
 
@@ -288,70 +406,37 @@ __device__ __forceinline__ void pair_tile(int tile, int num_m, int num_n, int& m
   nb = idx / bm;
 }
 
-// 32 neighbouring outputs of one row.  cs: the columns' scale, bias and gate (128 floats apart) in
-// shared memory, read by all lanes at once.
+// The outputs of one channel for 32 tokens from m on, `tokens` of them inside C.
 template <bool RESID, bool BF16OUT>
-__device__ __forceinline__ void store_row32(const GemmI8Params& p, const uint32_t (&acc)[32], float sa, int row, int col,
-                                            const float* cs, bool vec) {
-  float v[32];
+__device__ __forceinline__ void store_channel32(const GemmI8Params& p, const uint32_t (&acc)[32], const I8Channel& ch,
+                                                int m, int tokens, int n) {
+  const int64_t at = static_cast<int64_t>(m) * p.N + n;
+  float res[32];
+  if constexpr (RESID) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float4 sc = *reinterpret_cast<const float4*>(cs + 4 * i);
-    const float4 bi = *reinterpret_cast<const float4*>(cs + 128 + 4 * i);
-    v[4 * i] = fmaf(__int2float_rn(static_cast<int>(acc[4 * i])) * sa, sc.x, bi.x);
-    v[4 * i + 1] = fmaf(__int2float_rn(static_cast<int>(acc[4 * i + 1])) * sa, sc.y, bi.y);
-    v[4 * i + 2] = fmaf(__int2float_rn(static_cast<int>(acc[4 * i + 2])) * sa, sc.z, bi.z);
-    v[4 * i + 3] = fmaf(__int2float_rn(static_cast<int>(acc[4 * i + 3])) * sa, sc.w, bi.w);
+    for (int i = 0; i < 32; ++i) res[i] = i < tokens ? p.residual[at + static_cast<int64_t>(i) * p.N] : 0.f;
   }
-  const int64_t at = static_cast<int64_t>(row) * p.N + col;
-  if (vec) {
-    if constexpr (RESID) {
-      const float4* r = reinterpret_cast<const float4*>(p.residual + at);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 x = r[i];
-        const float4 g = *reinterpret_cast<const float4*>(cs + 256 + 4 * i);
-        v[4 * i] = fmaf(g.x, v[4 * i], x.x);
-        v[4 * i + 1] = fmaf(g.y, v[4 * i + 1], x.y);
-        v[4 * i + 2] = fmaf(g.z, v[4 * i + 2], x.z);
-        v[4 * i + 3] = fmaf(g.w, v[4 * i + 3], x.w);
-      }
-    }
-    if constexpr (BF16OUT) {
-      uint4* d = reinterpret_cast<uint4*>(static_cast<bf16*>(p.c) + at);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        d[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                          pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
-    } else {
-      float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.c) + at);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (col + i >= p.N) continue;
-      float y = v[i];
-      if constexpr (RESID) y = fmaf(cs[256 + i], y, p.residual[at + i]);
-      if constexpr (BF16OUT)
-        static_cast<bf16*>(p.c)[at + i] = __float2bfloat16_rn(y);
-      else
-        static_cast<float*>(p.c)[at + i] = y;
-    }
+  for (int i = 0; i < 32; ++i) {
+    if (i >= tokens) continue;
+    float v = fmaf(__int2float_rn(static_cast<int>(acc[i])) * __ldg(p.a_scale + m + i), ch.scale, ch.bias);
+    if constexpr (RESID) v = fmaf(ch.gate, v, res[i]);
+    if constexpr (BF16OUT)
+      static_cast<bf16*>(p.c)[at + static_cast<int64_t>(i) * p.N] = __float2bfloat16_rn(v);
+    else
+      static_cast<float*>(p.c)[at + static_cast<int64_t>(i) * p.N] = v;
   }
 }
 
 template <bool RESID, bool BF16OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+    gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                         const GemmI8Params p, unsigned* err) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sA = smem;
-  uint8_t* sB = smem + kPairStages * kPairOpBytes;
-  float* sCol = reinterpret_cast<float*>(smem + kPairStages * kPairStageBytes);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairStages * kPairStageBytes + kPairColBytes);
+  uint8_t* sW = smem;
+  uint8_t* sX = smem + kPairStages * kPairOpBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairStages * kPairStageBytes);
   uint64_t* empty = full + kPairStages;
   uint64_t* tfull = empty + kPairStages;
   uint64_t* tempty = tfull + 2;
@@ -384,8 +469,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -408,7 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
         int mb, nb;
         pair_tile(tile, num_m, num_n, mb, nb);
-        const int arow = mb * 256 + static_cast<int>(rank) * 128, brow = nb * 256 + static_cast<int>(rank) * 128;
+        const int wrow = nb * 256 + static_cast<int>(rank) * 128, xrow = mb * 256 + static_cast<int>(rank) * 128;
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, err, kErrGemmI8Producer, abort_flag)) {
             ok = false;
@@ -419,8 +504,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             armed[stage] = static_cast<int>(phase);
             mbar_arrive_expect_tx(&full[stage], 2 * kPairStageBytes);
           }
-          tma_load_2d_pair(sA + stage * kPairOpBytes, &tmA, full_leader, kb * kBK, arow);
-          tma_load_2d_pair(sB + stage * kPairOpBytes, &tmB, full_leader, kb * kBK, brow);
+          tma_load_2d_pair(sW + stage * kPairOpBytes, &tmW, full_leader, kb * kBK, wrow);
+          tma_load_2d_pair(sX + stage * kPairOpBytes, &tmX, full_leader, kb * kBK, xrow);
           if (++stage == kPairStages) {
             stage = 0;
             phase ^= 1;
@@ -447,11 +532,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + stage * kPairOpBytes);
-          const uint32_t b0 = smem_u32(sB + stage * kPairOpBytes);
+          const uint32_t w0 = smem_u32(sW + stage * kPairOpBytes);
+          const uint32_t x0 = smem_u32(sX + stage * kPairOpBytes);
 #pragma unroll
           for (int k = 0; k < kBK / 32; ++k)
-            mma_i8_ss_pair(d_tmem, sdesc_sw128(a0 + k * 32, 16, 1024), sdesc_sw128(b0 + k * 32, 16, 1024), kIdesc,
+            mma_i8_ss_pair(d_tmem, sdesc_sw128(w0 + k * 32, 16, 1024), sdesc_sw128(x0 + k * 32, 16, 1024), kIdesc,
                            (kb | k) != 0 ? 1u : 0u);
           tc_commit_pair_both(&empty[stage], 0x3);  // the slot in both CTAs
           if (++stage == kPairStages) {
@@ -471,40 +556,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else {
     const int quad = warp & 3;          // TMEM lane quadrant this warp may access
-    const int half = (warp - 2) >> 2;   // which half of the tile's columns it owns
-    float* cs = sCol + (warp - 2) * 384;
-    const bool rows16 = p.N % (BF16OUT ? 8 : 4) == 0;  // rows of C start on 16 bytes
+    const int half = (warp - 2) >> 2;   // which half of the tile's tokens it owns
     int it = 0;
     for (int tile = pair; tile < num_tiles; tile += num_pairs, ++it) {
       int mb, nb;
       pair_tile(tile, num_m, num_n, mb, nb);
       const int acc = it & 1;
-      const int row = mb * 256 + static_cast<int>(rank) * 128 + quad * 32 + lane;
-      const int col0 = nb * 256 + half * 128;
+      const int n = nb * 256 + static_cast<int>(rank) * 128 + quad * 32 + lane;  // the thread's channel
+      const int m0 = mb * 256 + half * 128;
       // Operands of the epilogue that do not depend on the accumulator are fetched first.
-      const float sa = row < p.M ? __ldg(p.a_scale + row) : 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = lane + 32 * i, n = col0 + c;
-        const bool in = n < p.N;
-        cs[c] = in ? __ldg(p.b_scale + n) : 0.f;
-        cs[128 + c] = in && p.bias ? __bfloat162float(p.bias[n]) : 0.f;
-        if constexpr (RESID) cs[256 + c] = in ? __ldg(p.gate + n) : 0.f;
+      I8Channel ch = {0.f, 0.f, 0.f};
+      if (n < p.N) {
+        ch.scale = __ldg(p.b_scale + n);
+        if (p.bias) ch.bias = __bfloat162float(p.bias[n]);
+        if constexpr (RESID) ch.gate = __ldg(p.gate + n);
       }
-      __syncwarp();
+      if constexpr (RESID) {
+        // The warp's part of the residual (32 channels of 128 tokens, a line each) comes to L2 meanwhile.
+        const int n0 = n - lane;
+#pragma unroll
+        for (int i = 0; i < 128; i += 32)
+          if (n0 < p.N && m0 + lane + i < p.M)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.residual + static_cast<int64_t>(m0 + lane + i) * p.N + n0));
+      }
       const bool ok = mbar_wait(&tfull[acc], (it >> 1) & 1, err, kErrGemmI8Epilogue, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) break;  // warp-uniform: TMEM loads are .sync.aligned
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * 128;
-#pragma unroll
-      for (int c = 0; c < 128; c += 32) {
-        if (col0 + c >= p.N) break;  // warp-uniform
+#pragma unroll 1
+      for (int c = 0; c < 128 && m0 + c < p.M; c += 32) {
         uint32_t v[32];
         tmem_ld32(tb + c, v);
-        if (row < p.M) store_row32<RESID, BF16OUT>(p, v, sa, row, col0 + c, cs + c, rows16 && col0 + c + 32 <= p.N);
+        const int tokens = p.M - m0 - c;
+        if (n < p.N) {
+          if (tokens >= 32)
+            store_channel32<RESID, BF16OUT>(p, v, ch, m0 + c, 32, n);
+          else
+            store_channel32<RESID, BF16OUT>(p, v, ch, m0 + c, tokens, n);
+        }
       }
       tc_fence_before();
-      __syncwarp();  // also: every lane is done with cs before the next tile's columns overwrite it
+      __syncwarp();
       if (lane == 0) {
         if (leader)
           mbar_arrive(&tempty[acc]);
@@ -533,12 +625,12 @@ cudaError_t launch_pair(const int8_t* a, const int8_t* b, const GemmI8Params& p,
     if (e != cudaSuccess) return e;
     mark_configured_on_device(configured);
   }
-  CUtensorMap ta, tb;
-  if (!make_tmap_i8_2d(&ta, a, p.K, p.M, kBK, 128, emsg) || !make_tmap_i8_2d(&tb, b, p.K, p.N, kBK, 128, emsg))
+  CUtensorMap tw, tx;
+  if (!make_tmap_i8_2d(&tw, b, p.K, p.N, kBK, 128, emsg) || !make_tmap_i8_2d(&tx, a, p.K, p.M, kBK, 128, emsg))
     return cudaErrorInvalidValue;
   const int64_t tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + 255) / 256);
   const int pairs = static_cast<int>(tiles < num_sms() / 2 ? tiles : num_sms() / 2);
-  gemm_i8_pair_kernel<RESID, BF16OUT><<<2 * pairs, kPairThreads, kPairSmemBytes, s>>>(ta, tb, p, err);
+  gemm_i8_pair_kernel<RESID, BF16OUT><<<2 * pairs, kPairThreads, kPairSmemBytes, s>>>(tw, tx, p, err);
   return cudaGetLastError();
 }
 
@@ -546,22 +638,18 @@ cudaError_t launch_pair(const int8_t* a, const int8_t* b, const GemmI8Params& p,
 
 cudaError_t launch_gemm_i8(const int8_t* a, const int8_t* b, const GemmI8Params& p, cudaStream_t s, unsigned* err,
                            std::string* emsg) {
-  if (p.M > 256) {
+  if (p.M <= 8) return launch_dot(a, b, p, s);
+  if (p.M > 128) {
     if (p.residual) return launch_pair<true, false>(a, b, p, s, err, emsg);
     return p.c_bf16 ? launch_pair<false, true>(a, b, p, s, err, emsg) : launch_pair<false, false>(a, b, p, s, err, emsg);
   }
-  const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : p.M <= 128 ? 128 : 256;
-  const int64_t tiles = static_cast<int64_t>((p.N + kTileN - 1) / kTileN) * ((p.M + nt - 1) / nt);
+  const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  const int64_t tiles = (p.N + kTileN - 1) / kTileN;
+  const int64_t slots = static_cast<int64_t>(num_sms()) * (nt <= 64 ? 2 : 1);
   const int num_kb = (p.K + kBK - 1) / kBK;
   int split = 1;
-  while (split < kMaxSplit && tiles * (split + 1) <= num_sms() && split + 1 <= num_kb) ++split;
-  switch (nt) {
-    case 16: return launch_flat<16>(a, b, p, split, s, err, emsg);
-    case 32: return launch_flat<32>(a, b, p, split, s, err, emsg);
-    case 64: return launch_flat<64>(a, b, p, split, s, err, emsg);
-    case 128: return launch_flat<128>(a, b, p, split, s, err, emsg);
-    default: return launch_flat<256>(a, b, p, split, s, err, emsg);
-  }
+  while (split < kMaxSplit && tiles * split * 2 <= slots && split * 2 <= num_kb) split *= 2;
+  return launch_flat_nt(nt, a, b, p, split, s, err, emsg);
 }
 
 }  // namespace moss
