@@ -15,7 +15,7 @@
 // sums meet in shared memory of the cluster (integers: the order does not matter).
 //   warp 0      TMA producer: 128 x 128 bytes of B and NT x 128 bytes of A per slot (128-byte swizzle)
 //   warp 1      MMA issuer, four 32-deep steps a slot
-//   warps 2..5  epilogue (one per TMEM lane quadrant)
+//   warps 2..9  epilogue (two per TMEM lane quadrant, each half of the tokens)
 #include "common.cuh"
 #include "internal.h"
 
@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kBK = 128;      // K bytes (= elements) per slot, one 128-byte swizzle row
 constexpr int kTileN = 128;   // output channels per tile
-constexpr int kFlatThreads = 192;
+constexpr int kFlatThreads = 320;
 constexpr int kMaxSplit = 8;  // portable cluster size
 static_assert(static_cast<int64_t>(kMaxI8K) * 128 * 128 <= (int64_t{1} << 30), "32-bit sums are exact");
 
@@ -35,12 +35,11 @@ struct FlatShape {
   static constexpr int kXBytes = NT * kBK;
   static constexpr int kStageBytes = kWBytes + kXBytes;
   static constexpr int kPartBytes = kTileN * NT * 4;  // partial sums a CTA receives from its cluster
-  // Two CTAs a SM up to 64 tokens, one above.
-  static constexpr int kCtas = NT <= 64 ? 2 : 1;
-  static constexpr int kStages = ((kCtas == 2 ? 111 : 224) * 1024 - kPartBytes) / kStageBytes;
+  static constexpr int kMaxStages = (223 * 1024 - kPartBytes) / kStageBytes;
+  static constexpr int kStages = kMaxStages < 10 ? kMaxStages : 10;
   static constexpr int kTmemCols = NT < 32 ? 32 : NT;
   static constexpr int kSmemBytes = kStages * kStageBytes + kPartBytes + NT * 4 + 1024 + 256;
-  static_assert(kStages >= 3 && kStageBytes % 1024 == 0 && kCtas * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
+  static_assert(kStageBytes % 1024 == 0 && kSmemBytes <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
@@ -76,8 +75,33 @@ __device__ __forceinline__ void store_value(const GemmI8Params& p, const I8Chann
     static_cast<float*>(p.c)[at] = v;
 }
 
+// The same for 16 tokens from m on, `count` of them inside C: every load before the first store.
+__device__ __forceinline__ void store_values16(const GemmI8Params& p, const I8Channel& ch, const uint32_t (&acc)[16],
+                                               const float* scales, int m, int count, int n) {
+  const int64_t at = static_cast<int64_t>(m) * p.N + n;
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = fmaf(__int2float_rn(static_cast<int>(acc[i])) * scales[i], ch.scale, ch.bias);
+  if (p.residual) {
+    float r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = i < count ? p.residual[at + static_cast<int64_t>(i) * p.N] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = fmaf(ch.gate, v[i], r[i]);
+  }
+  if (p.c_bf16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < count) static_cast<bf16*>(p.c)[at + static_cast<int64_t>(i) * p.N] = __float2bfloat16_rn(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < count) static_cast<float*>(p.c)[at + static_cast<int64_t>(i) * p.N] = v[i];
+  }
+}
+
 template <int NT>
-__global__ void __launch_bounds__(kFlatThreads, FlatShape<NT>::kCtas)
+__global__ void __launch_bounds__(kFlatThreads, 1)
     gemm_i8_flat_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                         const GemmI8Params p, int split, unsigned* err) {
   using S = FlatShape<NT>;
@@ -112,19 +136,23 @@ __global__ void __launch_bounds__(kFlatThreads, FlatShape<NT>::kCtas)
     mbar_init(tfull, 1);
     *abort_flag = 0;
     fence_mbar_init();
-  }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmX);
+    fence_proxy_async_smem();
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, S::kTmemCols);
     tmem_relinquish();
   }
+  // The producer warp needs neither TMEM nor the others: it announces its barriers and goes on, so the
+  // first loads are under way while TMEM is allocated (about 0.7 us of a call of 7).
   tc_fence_before();
-  __syncthreads();
+  if (warp == 0) {
+    __syncwarp();
+    asm volatile("bar.arrive 2, %0;" ::"n"(kFlatThreads) : "memory");
+  } else {
+    asm volatile("bar.sync 2, %0;" ::"n"(kFlatThreads) : "memory");
+  }
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = warp == 0 ? 0u : *tmem_slot;
   if (split > 1) cluster_arrive();
 
   if (warp == 0) {
@@ -179,6 +207,7 @@ __global__ void __launch_bounds__(kFlatThreads, FlatShape<NT>::kCtas)
   const int quad = warp & 3;  // TMEM lane quadrant of an epilogue warp
   const int ln = quad * 32 + lane;
   const int n = n0 + ln;
+  const int half = (warp - 2) >> 2;  // its half of the tokens
   const bool epi = warp >= 2;
   bool ok = false;
   I8Channel ch = {0.f, 0.f, 0.f};
@@ -189,8 +218,8 @@ __global__ void __launch_bounds__(kFlatThreads, FlatShape<NT>::kCtas)
       if (p.bias) ch.bias = __bfloat162float(p.bias[n]);
       if (p.gate) ch.gate = __ldg(p.gate + n);
     }
-    for (int i = ln; i < NT; i += 128) scales[i] = m0 + i < p.M ? __ldg(p.a_scale + m0 + i) : 0.f;
-    asm volatile("bar.sync 1, 128;" ::: "memory");  // the four epilogue warps
+    for (int i = half * 128 + ln; i < NT; i += 256) scales[i] = m0 + i < p.M ? __ldg(p.a_scale + m0 + i) : 0.f;
+    asm volatile("bar.sync 1, 256;" ::: "memory");  // the eight epilogue warps
     ok = mbar_wait(tfull, 0, err, kErrGemmI8Epilogue, abort_flag) && !*abort_flag;
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
@@ -198,14 +227,10 @@ __global__ void __launch_bounds__(kFlatThreads, FlatShape<NT>::kCtas)
   if (split == 1) {
     if (epi && ok) {
 #pragma unroll 1
-      for (int c = 0; c < NT && m0 + c < p.M; c += 16) {
+      for (int c = half * 16; c < NT && m0 + c < p.M; c += 32) {
         uint32_t v[16];
         tmem_ld16(tb + c, v);
-        if (n < p.N) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (m0 + c + i < p.M) store_value(p, ch, static_cast<int>(v[i]), scales[c + i], m0 + c + i, n);
-        }
+        if (n < p.N) store_values16(p, ch, v, scales + c, m0 + c, min(16, p.M - m0 - c), n);
       }
     }
   } else {
@@ -218,7 +243,7 @@ __global__ void __launch_bounds__(kFlatThreads, FlatShape<NT>::kCtas)
     if (epi && ok) {
       const uint32_t mine = smem_u32(part + rank * share * kTileN + ln);
 #pragma unroll 1
-      for (int c = 0; c < tokens; c += 16) {
+      for (int c = half * 16; c < tokens; c += 32) {
         uint32_t v[16];
         tmem_ld16(tb + c, v);
 #pragma unroll
@@ -231,12 +256,18 @@ __global__ void __launch_bounds__(kFlatThreads, FlatShape<NT>::kCtas)
     cluster_sync();
     if (epi && ok && n < p.N) {
       const int c0 = rank * share, count = min(share, tokens - c0);
-#pragma unroll 4
-      for (int i = 0; i < count; ++i) {
-        uint32_t sum = 0;
-#pragma unroll 4
-        for (int r = 0; r < split; ++r) sum += part[(r * share + i) * kTileN + ln];
-        store_value(p, ch, static_cast<int>(sum), scales[c0 + i], m0 + c0 + i, n);
+      const int i1 = half ? count : min(count, (share + 1) / 2);
+#pragma unroll 1
+      for (int i0 = half ? (share + 1) / 2 : 0; i0 < i1; i0 += 16) {
+        uint32_t sum[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[i] = 0;
+#pragma unroll 1
+        for (int r = 0; r < split; ++r)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (i0 + i < i1) sum[i] += part[(r * share + i0 + i) * kTileN + ln];
+        store_values16(p, ch, sum, scales + c0 + i0, m0 + c0 + i0, min(16, i1 - i0), n);
       }
     }
   }
@@ -281,7 +312,6 @@ cudaError_t launch_flat(const int8_t* a, const int8_t* b, const GemmI8Params& p,
 cudaError_t launch_flat_nt(int nt, const int8_t* a, const int8_t* b, const GemmI8Params& p, int split, cudaStream_t s,
                            unsigned* err, std::string* emsg) {
   switch (nt) {
-    case 16: return launch_flat<16>(a, b, p, split, s, err, emsg);
     case 32: return launch_flat<32>(a, b, p, split, s, err, emsg);
     case 64: return launch_flat<64>(a, b, p, split, s, err, emsg);
     default: return launch_flat<128>(a, b, p, split, s, err, emsg);
@@ -289,107 +319,169 @@ cudaError_t launch_flat_nt(int nt, const int8_t* a, const int8_t* b, const GemmI
 }
 
 // ------------------------------------------------------------------------ a few tokens
-constexpr int kDotThreads = 256;
-constexpr int kDotWarps = kDotThreads / 32;
 
 // 16 bytes of weights, read once: past L1.
-__device__ __forceinline__ int4 ld_weights(const int4* p) {
+__device__ __forceinline__ int4 ld_weights(const int8_t* p) {
   int4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
 }
+// D (16 x 8) += A (16 x 32, rows) B (32 x 8, columns), 8-bit integers: a.x, a.z of row lane / 4 and a.y,
+// a.w of the row 8 below; b of column lane / 4; c[0..1] row lane / 4, columns 2 (lane % 4) + 0..1, c[2..3] 8 below.
+__device__ __forceinline__ void mma_16832(int (&c)[4], int a0, int a1, int a2, int a3, int b0, int b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// wk warps of a block (a power of two) share 16 channels and take K in turns of U x 64 bytes.
+template <int TG, int U, int W>
+__global__ void __launch_bounds__(32 * W) gemm_i8_few_kernel(const int8_t* __restrict__ a,
+                                                                   const int8_t* __restrict__ b, const GemmI8Params p,
+                                                                   int wk) {
+  __shared__ int part[W][TG * 8][16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, q = lane & 3;
+  const int sub = warp & (wk - 1);
+  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * (W / wk) + warp / wk) * 16;
+  const int8_t* w0 = b + (n0 + g < p.N ? n0 + g : p.N - 1) * p.K;
+  const int8_t* w1 = b + (n0 + g + 8 < p.N ? n0 + g + 8 : p.N - 1) * p.K;
+  const int8_t* x = a + static_cast<int64_t>(g) * p.K;
+  int acc[TG][4];
+#pragma unroll
+  for (int t = 0; t < TG; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0;
+  const int4 zero = make_int4(0, 0, 0, 0);
+  for (int k0 = sub * (U * 64); k0 < p.K; k0 += wk * (U * 64)) {
+    int4 wa[U], wb[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * 64 + q * 16;
+      wa[u] = k < p.K ? ld_weights(w0 + k) : zero;
+      wb[u] = k < p.K ? ld_weights(w1 + k) : zero;
+    }
+#pragma unroll
+    for (int t = 0; t < TG; ++t) {
+      int4 xv[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * 64 + q * 16;
+        xv[u] = k < p.K && t * 8 + g < p.M ? __ldg(reinterpret_cast<const int4*>(x + static_cast<int64_t>(t) * 8 * p.K + k)) : zero;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        mma_16832(acc[t], wa[u].x, wb[u].x, wa[u].y, wb[u].y, xv[u].x, xv[u].y);
+        mma_16832(acc[t], wa[u].z, wb[u].z, wa[u].w, wb[u].w, xv[u].z, xv[u].w);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TG; ++t) {
+    part[warp][t * 8 + 2 * q][g] = acc[t][0];
+    part[warp][t * 8 + 2 * q + 1][g] = acc[t][1];
+    part[warp][t * 8 + 2 * q][g + 8] = acc[t][2];
+    part[warp][t * 8 + 2 * q + 1][g + 8] = acc[t][3];
+  }
+  __syncthreads();
+  // The group's wk warps finish its 16 x M outputs: lane % 16 the channel.
+  const int64_t n = n0 + (lane & 15);
+  if (n >= p.N) return;
+  I8Channel ch = {__ldg(p.b_scale + n), 0.f, 0.f};
+  if (p.bias) ch.bias = __bfloat162float(p.bias[n]);
+  if (p.gate) ch.gate = __ldg(p.gate + n);
+  const int w_first = warp - sub;
+  for (int t = sub * 2 + (lane >> 4); t < p.M; t += 2 * wk) {
+    int sum = 0;
+    for (int k = 0; k < wk; ++k) sum += part[w_first + k][t][lane & 15];
+    store_value(p, ch, sum, __ldg(p.a_scale + t), t, static_cast<int>(n));
+  }
+}
+
+template <int TG, int U, int W>
+cudaError_t launch_few_u(const int8_t* a, const int8_t* b, const GemmI8Params& p, cudaStream_t s) {
+  int wk = 1;  // warps per group of 16 channels: K in one turn of each, if the block has so many
+  while (wk < W && p.K > U * 64 * wk) wk *= 2;
+  const int64_t groups = (static_cast<int64_t>(p.N) + 15) / 16;
+  gemm_i8_few_kernel<TG, U, W><<<static_cast<unsigned>((groups * wk + W - 1) / W), 32 * W, 0, s>>>(a, b, p, wk);
+  return cudaGetLastError();
+}
+template <int TG>
+cudaError_t launch_few(const int8_t* a, const int8_t* b, const GemmI8Params& p, cudaStream_t s) {
+  if (p.K <= 3072) return launch_few_u<TG, 6, 8>(a, b, p, s);
+  if (p.K <= 4096) return launch_few_u<TG, 8, 8>(a, b, p, s);
+  return launch_few_u<TG, 8, 16>(a, b, p, s);
+}
+
+// ------------------------------------------------------------------------ one token
+// A warp holds R channels, 16 bytes of each a lane and turn: whole 512-byte pieces of the rows.
+constexpr int kOneThreads = 256;
+constexpr int kOneWarps = kOneThreads / 32;
+constexpr int kOneRows = 8;
+
 __device__ __forceinline__ int dot16(const int4& a, const int4& b, int c) {
   return __dp4a(a.w, b.w, __dp4a(a.z, b.z, __dp4a(a.y, b.y, __dp4a(a.x, b.x, c))));
 }
 
-// wk warps of a block (a power of two) share R channels: each takes the 512-byte pieces wk apart.
-template <int MT, int R, int U>
-__global__ void __launch_bounds__(kDotThreads) gemm_i8_dot_kernel(const int8_t* __restrict__ a,
-                                                                   const int8_t* __restrict__ b, const GemmI8Params p,
-                                                                   int wk) {
-  __shared__ int part[kDotWarps][R * MT];
+__global__ void __launch_bounds__(kOneThreads) gemm_i8_one_kernel(const int8_t* __restrict__ a,
+                                                                  const int8_t* __restrict__ b, const GemmI8Params p,
+                                                                  int wk) {
+  constexpr int R = kOneRows;
+  __shared__ int part[kOneWarps][R];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = warp / wk, sub = warp & (wk - 1);
-  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * (kDotWarps / wk) + group) * R;
-  const int chunks = p.K >> 4;  // 16-byte pieces of a row
-  const int4* w[R];
+  const int sub = warp & (wk - 1);
+  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * (kOneWarps / wk) + warp / wk) * R;
+  const int8_t* w[R];
+  int acc[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-    w[r] = reinterpret_cast<const int4*>(b + (n0 + r < p.N ? n0 + r : p.N - 1) * p.K);
-  int acc[R][MT];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[r][t] = 0;
-  const int4 zero = make_int4(0, 0, 0, 0);
-  for (int c0 = sub * 32 + lane; c0 - lane < chunks; c0 += U * wk * 32) {
-    int4 wv[U][R];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int c = c0 + u * wk * 32;
-        wv[u][r] = c < chunks ? ld_weights(w[r] + c) : zero;
-      }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * wk * 32;
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const int4 x = c < chunks && t < p.M ? __ldg(reinterpret_cast<const int4*>(a + static_cast<int64_t>(t) * p.K) + c) : zero;
-#pragma unroll
-        for (int r = 0; r < R; ++r) acc[r][t] = dot16(wv[u][r], x, acc[r][t]);
-      }
-    }
+  for (int r = 0; r < R; ++r) {
+    w[r] = b + (n0 + r < p.N ? n0 + r : p.N - 1) * p.K;
+    acc[r] = 0;
   }
-  // Lane r * MT + t ends with the sum of channel r and token t.
-  int mine = 0;
+  for (int k = (sub * 32 + lane) * 16; k < p.K; k += wk * 512) {
+    int4 wv[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r) wv[r] = ld_weights(w[r] + k);
+    const int4 x = __ldg(reinterpret_cast<const int4*>(a + k));
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const int sum = __reduce_add_sync(0xffffffffu, acc[r][t]);
-      if (lane == r * MT + t) mine = sum;
-    }
+    for (int r = 0; r < R; ++r) acc[r] = dot16(wv[r], x, acc[r]);
+  }
+  __syncwarp();
+  int mine = 0;  // lane r: channel r
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int sum = __reduce_add_sync(0xffffffffu, acc[r]);
+    if (lane == r) mine = sum;
+  }
   if (wk > 1) {
-    if (lane < R * MT) part[warp][lane] = mine;
+    if (lane < R) part[warp][lane] = mine;
     __syncthreads();
     if (sub != 0) return;
     mine = 0;
-    if (lane < R * MT)
+    if (lane < R)
       for (int k = 0; k < wk; ++k) mine += part[warp + k][lane];
   }
-  const int64_t n = n0 + lane / MT;
-  const int t = lane % MT;
-  if (lane >= R * MT || n >= p.N || t >= p.M) return;
+  const int64_t n = n0 + lane;
+  if (lane >= R || n >= p.N) return;
   I8Channel ch = {__ldg(p.b_scale + n), 0.f, 0.f};
   if (p.bias) ch.bias = __bfloat162float(p.bias[n]);
   if (p.gate) ch.gate = __ldg(p.gate + n);
-  store_value(p, ch, mine, __ldg(p.a_scale + t), t, static_cast<int>(n));
+  store_value(p, ch, mine, __ldg(p.a_scale), 0, static_cast<int>(n));
 }
 
-template <int MT, int R, int U>
-cudaError_t launch_dot_mt(const int8_t* a, const int8_t* b, const GemmI8Params& p, cudaStream_t s) {
-  const int64_t groups = (static_cast<int64_t>(p.N) + R - 1) / R;
-  // Warps per group of channels: until every SM has two blocks, while each warp keeps a piece of K.
+cudaError_t launch_one(const int8_t* a, const int8_t* b, const GemmI8Params& p, cudaStream_t s) {
+  // Warps per group of channels: as many as leave the launch at 21 warps a SM, about one wave.
+  const int64_t groups = (static_cast<int64_t>(p.N) + kOneRows - 1) / kOneRows;
   int wk = 1;
-  while (wk < kDotWarps && groups * wk < static_cast<int64_t>(num_sms()) * 2 * kDotWarps && p.K > 512 * wk) wk *= 2;
-  const unsigned grid = static_cast<unsigned>((groups * wk + kDotWarps - 1) / kDotWarps);
-  gemm_i8_dot_kernel<MT, R, U><<<grid, kDotThreads, 0, s>>>(a, b, p, wk);
+  while (wk < kOneWarps && groups * wk * 2 <= static_cast<int64_t>(num_sms()) * 21 && p.K > 512 * wk) wk *= 2;
+  gemm_i8_one_kernel<<<static_cast<unsigned>((groups * wk + kOneWarps - 1) / kOneWarps), kOneThreads, 0, s>>>(a, b, p, wk);
   return cudaGetLastError();
-}
-
-cudaError_t launch_dot(const int8_t* a, const int8_t* b, const GemmI8Params& p, cudaStream_t s) {
-  if (p.M == 1) return launch_dot_mt<1, 4, 2>(a, b, p, s);
-  if (p.M == 2) return launch_dot_mt<2, 4, 2>(a, b, p, s);
-  if (p.M <= 4) return launch_dot_mt<4, 4, 2>(a, b, p, s);
-  return launch_dot_mt<8, 4, 2>(a, b, p, s);
 }
 
 // ------------------------------------------------------------------------ CTA pairs
 constexpr int kPairThreads = 320;    // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
+
 constexpr int kPairStages = 6;
 constexpr int kPairOpBytes = 128 * kBK;                 // one operand's rows of one CTA in a slot
 constexpr int kPairStageBytes = 2 * kPairOpBytes;       // 32 KB
@@ -638,17 +730,18 @@ cudaError_t launch_pair(const int8_t* a, const int8_t* b, const GemmI8Params& p,
 
 cudaError_t launch_gemm_i8(const int8_t* a, const int8_t* b, const GemmI8Params& p, cudaStream_t s, unsigned* err,
                            std::string* emsg) {
-  if (p.M <= 8) return launch_dot(a, b, p, s);
-  if (p.M > 128) {
+  if (p.M == 1) return launch_one(a, b, p, s);
+  if (p.M <= 8) return launch_few<1>(a, b, p, s);
+  if (p.M <= 16 && p.N <= 8192) return launch_few<2>(a, b, p, s);
+  const int nt = p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  const int64_t tiles = static_cast<int64_t>((p.N + kTileN - 1) / kTileN) * ((p.M + nt - 1) / nt);
+  if (p.M > 128 && tiles > num_sms()) {
     if (p.residual) return launch_pair<true, false>(a, b, p, s, err, emsg);
     return p.c_bf16 ? launch_pair<false, true>(a, b, p, s, err, emsg) : launch_pair<false, false>(a, b, p, s, err, emsg);
   }
-  const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-  const int64_t tiles = (p.N + kTileN - 1) / kTileN;
-  const int64_t slots = static_cast<int64_t>(num_sms()) * (nt <= 64 ? 2 : 1);
   const int num_kb = (p.K + kBK - 1) / kBK;
   int split = 1;
-  while (split < kMaxSplit && tiles * split * 2 <= slots && split * 2 <= num_kb) split *= 2;
+  while (split < kMaxSplit && tiles * split * 2 <= num_sms() && split * 2 <= num_kb) split *= 2;
   return launch_flat_nt(nt, a, b, p, split, s, err, emsg);
 }
 
