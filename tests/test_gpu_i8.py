@@ -86,6 +86,23 @@ def test_quantize_halves(dtype):
         check_scale(scale, ref_scale)
 
 
+@pytest.mark.parametrize("e", [0, -50, -126, 112])
+def test_quantize_every_ratio_of_bf16_values(e):
+    """Every significand of the largest element against every significand of the others down to 2^-10 of it:
+    the rule that BF16 rows are rounded without a check holds for all of them."""
+    sig = torch.arange(128, 256, dtype=torch.float64, device="cuda")
+    amax = sig[:, None] * 2.0 ** e
+    others = (sig[None, :] * 2.0 ** -torch.arange(0, 11, dtype=torch.float64, device="cuda")[:, None]).reshape(1, -1) * 2.0 ** e
+    x = torch.where(others <= amax, others, torch.zeros_like(others))
+    x = torch.cat([amax, x, -x, torch.zeros(128, 15, dtype=torch.float64, device="cuda")], dim=1)
+    xb = x.to(torch.bfloat16)
+    assert torch.equal(xb.double(), x) or e < -100
+    q, scale = moss.op_quantize_i8(xb)
+    ref, ref_scale = quantized(xb.double())
+    assert torch.equal(q.double(), ref)
+    check_scale(scale, ref_scale)
+
+
 def test_quantize_extremes():
     """Subnormal rows, the largest finite values, one element set, and rows that are not finite."""
     tiny, big = 2.0 ** -149, float(np.finfo(np.float32).max)
@@ -130,7 +147,8 @@ def test_rows_with_a_stride_and_their_surroundings():
 
 def check_rows_of(q, scale, h, err):
     """q * scale against h (float64), where the kernel's FP32 rows are within err of h: an element is off by
-    its own error, half a step (of a scale that the largest error moved) and FP32's rounding."""
+    its own error, half a step (of a scale that the largest error moved) and FP32's roundings of 127 / amax
+    and of the scale, u of the element each."""
     amax = h.abs().amax(dim=1)
     emax = err.amax(dim=1)
     assert ((scale.double() - amax / 127).abs() <= emax / 127 + 2 * U * amax / 127).all()
