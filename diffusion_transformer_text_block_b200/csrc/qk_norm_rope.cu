@@ -11,7 +11,8 @@
 // a lane, always the same 8 of a head: with halves a lane's elements are 4 of the first half and the
 // 4 they pair with, so no pairing needs a shuffle.  A warp stays on one token and walks over some of
 // its heads, so a lane reads its gains and angles once and folds them into 16 coefficients:
-// (g_a cos, g_b sin, g_a sin, g_b cos) per pair, 3 operations an element after the sum of squares.
+// (g_a cos, -g_b sin, g_a sin, g_b cos) per pair.  The first and the second elements of the pairs are
+// kept apart, so that all the arithmetic goes two pairs an instruction.
 #include "common.cuh"
 #include "internal.h"
 
@@ -22,40 +23,81 @@ namespace {
 constexpr int kQkThreads = 256;
 constexpr int kQkUnroll = 4;  // heads in flight per lane group
 
-__device__ __forceinline__ void load4(const float* p, float* v) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-}
-__device__ __forceinline__ void load4(const bf16* p, float* v) {
-  const uint2 a = *reinterpret_cast<const uint2*>(p);
-  v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
-  v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
-}
-__device__ __forceinline__ void load8(const float* p, float* v) { load4(p, v); load4(p + 4, v + 4); }
-__device__ __forceinline__ void load8(const bf16* p, float* v) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// A lane's 8 elements as they lie in memory (two pieces of 4), and apart: a, the pairs' first elements, and
+// b, their second ones.
+template <typename T>
+struct Piece;
+template <>
+struct Piece<float> {
+  float4 x, y;
+  template <bool HALVES>
+  __device__ __forceinline__ void load(const float* p, int o1, int o2) {
+    x = *reinterpret_cast<const float4*>(p + o1);
+    y = *reinterpret_cast<const float4*>(p + o2);
   }
-}
-__device__ __forceinline__ void store4(float* p, const float* v) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-__device__ __forceinline__ void store4(bf16* p, const float* v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-}
-__device__ __forceinline__ void store8(float* p, const float* v) { store4(p, v); store4(p + 4, v + 4); }
-__device__ __forceinline__ void store8(bf16* p, const float* v) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
+  template <bool HALVES>
+  __device__ __forceinline__ void split(float2 (&a)[2], float2 (&b)[2]) const {
+    if (HALVES) {
+      a[0] = make_float2(x.x, x.y); a[1] = make_float2(x.z, x.w);
+      b[0] = make_float2(y.x, y.y); b[1] = make_float2(y.z, y.w);
+    } else {
+      a[0] = make_float2(x.x, x.z); a[1] = make_float2(y.x, y.z);
+      b[0] = make_float2(x.y, x.w); b[1] = make_float2(y.y, y.w);
+    }
+  }
+  template <bool HALVES>
+  static __device__ __forceinline__ void store(float* p, int o1, int o2, const float2 (&a)[2], const float2 (&b)[2]) {
+    float4* d1 = reinterpret_cast<float4*>(p + o1);
+    float4* d2 = reinterpret_cast<float4*>(p + o2);
+    if (HALVES) {
+      *d1 = make_float4(a[0].x, a[0].y, a[1].x, a[1].y);
+      *d2 = make_float4(b[0].x, b[0].y, b[1].x, b[1].y);
+    } else {
+      *d1 = make_float4(a[0].x, b[0].x, a[0].y, b[0].y);
+      *d2 = make_float4(a[1].x, b[1].x, a[1].y, b[1].y);
+    }
+  }
+};
+template <>
+struct Piece<bf16> {
+  uint4 w;
+  template <bool HALVES>
+  __device__ __forceinline__ void load(const bf16* p, int o1, int o2) {
+    if (HALVES) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p + o1), y = *reinterpret_cast<const uint2*>(p + o2);
+      w = make_uint4(x.x, x.y, y.x, y.y);
+    } else {
+      w = *reinterpret_cast<const uint4*>(p + o1);
+    }
+  }
+  template <bool HALVES>
+  __device__ __forceinline__ void split(float2 (&a)[2], float2 (&b)[2]) const {
+    if (HALVES) {
+      a[0] = make_float2(lo_bf16(w.x), hi_bf16(w.x)); a[1] = make_float2(lo_bf16(w.y), hi_bf16(w.y));
+      b[0] = make_float2(lo_bf16(w.z), hi_bf16(w.z)); b[1] = make_float2(lo_bf16(w.w), hi_bf16(w.w));
+    } else {
+      a[0] = make_float2(lo_bf16(w.x), lo_bf16(w.y)); a[1] = make_float2(lo_bf16(w.z), lo_bf16(w.w));
+      b[0] = make_float2(hi_bf16(w.x), hi_bf16(w.y)); b[1] = make_float2(hi_bf16(w.z), hi_bf16(w.w));
+    }
+  }
+  template <bool HALVES>
+  static __device__ __forceinline__ void store(bf16* p, int o1, int o2, const float2 (&a)[2], const float2 (&b)[2]) {
+    if (HALVES) {
+      *reinterpret_cast<uint2*>(p + o1) = make_uint2(pack_bf16x2(a[0].x, a[0].y), pack_bf16x2(a[1].x, a[1].y));
+      *reinterpret_cast<uint2*>(p + o2) = make_uint2(pack_bf16x2(b[0].x, b[0].y), pack_bf16x2(b[1].x, b[1].y));
+    } else {
+      *reinterpret_cast<uint4*>(p + o1) = make_uint4(pack_bf16x2(a[0].x, b[0].x), pack_bf16x2(a[0].y, b[0].y),
+                                                     pack_bf16x2(a[1].x, b[1].x), pack_bf16x2(a[1].y, b[1].y));
+    }
+  }
+};
 
 // LPH lanes per head (head_dim = 8 LPH).
 template <int LPH, bool HALVES, typename TI, typename TO>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkNormRopeParams p, unsigned* err) {
+__global__ void __launch_bounds__(kQkThreads, 4) qk_norm_rope_kernel(const QkNormRopeParams p, unsigned* err) {
   constexpr int kDim = 8 * LPH;
   constexpr int kPer = 32 / LPH;  // heads a warp works on at once
   const int lane = threadIdx.x & 31;
@@ -85,73 +127,62 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkNormRo
     o1 = 4 * l;
     o2 = p.rot_dim / 2 + 4 * l;
   }
-  float g[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-  const float* gain = is_q ? p.q_gain : p.k_gain;
-  if (gain) {
-    load4(gain + o1, g);
-    load4(gain + o2, g + 4);
-  }
-  // Pair i of the lane: elements (2i, 2i + 1), or with halves (i, i + 4).
-  float ca[4], sb[4], sa[4], cb[4];
+  // Coefficients of the lane's 4 pairs, two a register pair: y_a = a ca + b sb, y_b = a sa + b cb.
+  float2 ca[2], sb[2], sa[2], cb[2];
   {
-    float t[8] = {1.f, 0.f, 1.f, 0.f, 1.f, 0.f, 1.f, 0.f};
-    if (turned) load8(p.rope + (static_cast<int64_t>(pos) * (p.rot_dim / 2) + 4 * l) * 2, t);
+    Piece<float> g = {make_float4(1.f, 1.f, 1.f, 1.f), make_float4(1.f, 1.f, 1.f, 1.f)};
+    const float* gain = is_q ? p.q_gain : p.k_gain;
+    if (gain) g.load<HALVES>(gain, o1, o2);
+    float2 ga[2], gb[2];
+    g.split<HALVES>(ga, gb);
+    Piece<float> t = {make_float4(1.f, 0.f, 1.f, 0.f), make_float4(1.f, 0.f, 1.f, 0.f)};  // (cos, sin) of 4 pairs
+    const float* angles = p.rope + (static_cast<int64_t>(pos) * (p.rot_dim / 2) + 4 * l) * 2;
+    if (turned) t.load<false>(angles, 0, 4);
+    float2 c[2], s[2];
+    t.split<false>(c, s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int a = HALVES ? i : 2 * i, b = HALVES ? i + 4 : 2 * i + 1;
-      ca[i] = g[a] * t[2 * i];
-      sb[i] = g[b] * t[2 * i + 1];
-      sa[i] = g[a] * t[2 * i + 1];
-      cb[i] = g[b] * t[2 * i];
+    for (int i = 0; i < 2; ++i) {
+      ca[i] = __fmul2_rn(ga[i], c[i]);
+      sa[i] = __fmul2_rn(ga[i], s[i]);
+      cb[i] = __fmul2_rn(gb[i], c[i]);
+      sb[i] = __fmul2_rn(gb[i], make_float2(-s[i].x, -s[i].y));
     }
   }
   const int h_end = min(heads, (chunk + 1) * p.heads_per_chunk);
-  for (int h0 = chunk * p.heads_per_chunk + lane / LPH; h0 - lane / LPH < h_end; h0 += kPer * kQkUnroll) {
-    float v[kQkUnroll][8];
+  const int group = lane / LPH;  // the lane's head among the kPer of a step
+  // kQkUnroll steps at once; `left` heads from the first on, only the last round has too few.
+  const auto round = [&](const TI* s, TO* d, int left) {
+    Piece<TI> v[kQkUnroll];
+#pragma unroll
+    for (int i = 0; i < kQkUnroll; ++i)
+      if (group + i * kPer < left) v[i].template load<HALVES>(s + i * kPer * kDim, o1, o2);
 #pragma unroll
     for (int i = 0; i < kQkUnroll; ++i) {
-      const int h = h0 + i * kPer;
-      if (h < h_end) {
-        const TI* s = src + static_cast<int64_t>(h) * kDim;
-        if (HALVES) {
-          load4(s + o1, v[i]);
-          load4(s + o2, v[i] + 4);
-        } else {
-          load8(s + o1, v[i]);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kQkUnroll; ++i) {
-      const int h = h0 + i * kPer;
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+      float2 a[2], b[2];
+      v[i].template split<HALVES>(a, b);
+      float2 q = __ffma2_rn(b[1], b[1], __ffma2_rn(b[0], b[0], __ffma2_rn(a[1], a[1], __fmul2_rn(a[0], a[0]))));
+      float ss = q.x + q.y;
 #pragma unroll
       for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       const float r = rsqrtf(fmaf(ss, 1.0f / kDim, p.eps));
-      float y[8];
+      const float2 rr = make_float2(r, r);
+      float2 ya[2], yb[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int a = HALVES ? j : 2 * j, b = HALVES ? j + 4 : 2 * j + 1;
-        const float xa = v[i][a] * r, xb = v[i][b] * r;
-        y[a] = fmaf(xa, ca[j], -(xb * sb[j]));
-        y[b] = fmaf(xa, sa[j], xb * cb[j]);
+      for (int j = 0; j < 2; ++j) {
+        a[j] = __fmul2_rn(a[j], rr);
+        b[j] = __fmul2_rn(b[j], rr);
+        ya[j] = __ffma2_rn(a[j], ca[j], __fmul2_rn(b[j], sb[j]));
+        yb[j] = __ffma2_rn(a[j], sa[j], __fmul2_rn(b[j], cb[j]));
       }
-      if (h < h_end) {
-        TO* d = dst + static_cast<int64_t>(h) * kDim;
-        if (HALVES) {
-          store4(d + o1, y);
-          store4(d + o2, y + 4);
-        } else {
-          store8(d + o1, y);
-        }
-      }
+      if (group + i * kPer < left) Piece<TO>::template store<HALVES>(d + i * kPer * kDim, o1, o2, ya, yb);
     }
-  }
+  };
+  int h = chunk * p.heads_per_chunk;
+  src += static_cast<int64_t>(h + group) * kDim;
+  dst += static_cast<int64_t>(h + group) * kDim;
+  constexpr int kRound = kPer * kQkUnroll;
+  for (; h + kRound <= h_end; h += kRound, src += kRound * kDim, dst += kRound * kDim) round(src, dst, kRound);
+  if (h < h_end) round(src, dst, h_end - h);
 }
 
 template <int LPH, bool HALVES, typename TI, typename TO>
