@@ -320,11 +320,28 @@ def _dtype_code(t, name):
     raise MossError(1, f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
 
 
+def _new(ref, shape, dtype, stream):
+    """A new tensor beside ref, from the pool of the stream that the call runs on (None: the current one)."""
+    if stream is None:
+        return ref.new_empty(shape, dtype=dtype)
+    if not isinstance(stream, _torch.cuda.Stream):
+        stream = _torch.cuda.ExternalStream(_stream(stream), device=ref.device)
+    with _torch.cuda.stream(stream):
+        return ref.new_empty(shape, dtype=dtype)
+
+
+def _int32(*sizes):
+    """The C calls take sizes as 32-bit integers."""
+    if max(sizes) > 0x7fffffff:
+        raise MossError(1, "a size does not fit 32 bits")
+
+
 def _rows_of(t, name):
     """(rows, width, stride between rows) of a 2-D tensor whose rows are contiguous."""
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise MossError(1, f"{name} must be [rows, dim] with contiguous rows")
     rows, width = t.shape
+    _int32(rows, width)
     return rows, width, t.stride(0) if rows > 1 else width
 
 
@@ -335,8 +352,8 @@ def op_quantize_i8(x, stream=None):
     _placed(x, dev, None, "x")
     code = _dtype_code(x, "x")
     rows, dim, stride = _rows_of(x, "x")
-    q = x.new_empty((rows, dim), dtype=torch.int8)
-    scale = x.new_empty(rows, dtype=torch.float32)
+    q = _new(x, (rows, dim), torch.int8, stream)
+    scale = _new(x, rows, torch.float32, stream)
     _check(lib().moss_op_quantize_i8(x.data_ptr(), code, stride, q.data_ptr(), scale.data_ptr(), rows, dim,
                                      _raw_stream(stream, dev)))
     return q, scale
@@ -346,9 +363,10 @@ def op_ln_modulate_i8(x, shift, scale, stream=None):
     """LN(x) (1 + scale) + shift of FP32 x [rows, dim], made 8-bit by rows: (q int8, q_scale FP32 [rows])."""
     torch, dev = _begin(x, "x")
     rows, dim = x.shape
+    _int32(rows, dim)
     f = torch.float32
-    q = x.new_empty((rows, dim), dtype=torch.int8)
-    q_scale = x.new_empty(rows)
+    q = _new(x, (rows, dim), torch.int8, stream)
+    q_scale = _new(x, rows, f, stream)
     _check(lib().moss_op_ln_modulate_i8(_arg(x, dev, f, x.shape, "x"), _arg(shift, dev, f, (dim,), "shift"),
                                         _arg(scale, dev, f, (dim,), "scale"), q.data_ptr(), q_scale.data_ptr(), rows,
                                         dim, _raw_stream(stream, dev)))
@@ -364,8 +382,8 @@ def op_swiglu_i8(gu, stream=None):
     if width % 2:
         raise MossError(1, "gu must hold gate and up halves of one width")
     dim = width // 2
-    q = gu.new_empty((rows, dim), dtype=torch.int8)
-    scale = gu.new_empty(rows, dtype=torch.float32)
+    q = _new(gu, (rows, dim), torch.int8, stream)
+    scale = _new(gu, rows, torch.float32, stream)
     _check(lib().moss_op_swiglu_i8(gu.data_ptr(), stride, q.data_ptr(), scale.data_ptr(), rows, dim,
                                    _raw_stream(stream, dev)))
     return q, scale
@@ -380,9 +398,10 @@ def op_gemm_i8(a, a_scale, b, b_scale, bias=None, gate=None, residual=None, out_
         raise MossError(1, "a must be [M, K] and b [N, K]")
     M, K = a.shape
     N = b.shape[0]
+    _int32(M, N, K)
     f, i8 = torch.float32, torch.int8
     if out is None:
-        out = a.new_empty((M, N), dtype=out_dtype or (f if residual is not None else torch.bfloat16))
+        out = _new(a, (M, N), out_dtype or (f if residual is not None else torch.bfloat16), stream)
     elif out_dtype is not None and out.dtype is not out_dtype:
         raise MossError(1, f"out is {out.dtype}, not {out_dtype}")
     _check(lib().moss_op_gemm_i8(
@@ -403,10 +422,10 @@ def _heads_of(t, dev, name):
     return shape, stride[0] if shape[0] > 1 else shape[1] * shape[2], t.data_ptr()
 
 
-def _heads_out(t, ref, shape, dtype, dev, name):
+def _heads_out(t, ref, shape, dtype, dev, stream, name):
     """(tensor, stride between tokens, address) of an output of ref's shape: t, or a new one."""
     if t is None:
-        t = ref.new_empty(shape, dtype=dtype)
+        t = _new(ref, shape, dtype, stream)
         return t, shape[1] * shape[2], t.data_ptr()
     out_shape, stride, ptr = _heads_of(t, dev, name)
     if out_shape != shape or t.dtype is not dtype:
@@ -431,14 +450,14 @@ def op_qk_norm_rope(q, k, q_gain, k_gain, rope, positions=None, pairing="adjacen
     shape, q_stride, q_ptr = _heads_of(q, dev, "q")
     rows, heads_q, d = shape
     want = out_dtype or (q_out.dtype if q_out is not None else torch.bfloat16)
-    q_out, qo_stride, qo_ptr = _heads_out(q_out, q, shape, want, dev, "q_out")
+    q_out, qo_stride, qo_ptr = _heads_out(q_out, q, shape, want, dev, stream, "q_out")
     heads_k, k_stride, ko_stride, k_ptr, ko_ptr = 0, 0, 0, 0, 0
     if k is not None:
         shape, k_stride, k_ptr = _heads_of(k, dev, "k")
         heads_k = shape[1]
         if shape[0] != rows or shape[2] != d or k.dtype is not q.dtype:
             raise MossError(1, "k must have q's tokens, head_dim and type")
-        k_out, ko_stride, ko_ptr = _heads_out(k_out, k, shape, want, dev, "k_out")
+        k_out, ko_stride, ko_ptr = _heads_out(k_out, k, shape, want, dev, stream, "k_out")
     elif k_out is not None or k_gain is not None:
         raise MossError(1, "k_out and k_gain go with k")
     n_pos, rot_dim, rope_ptr = 0, 0, None
@@ -448,6 +467,7 @@ def op_qk_norm_rope(q, k, q_gain, k_gain, rope, positions=None, pairing="adjacen
             raise MossError(1, "rope must be [n_pos, rot_dim/2, 2]")
         rope_ptr = _arg(rope, dev, f, shape, "rope")
         n_pos, rot_dim = shape[0], 2 * shape[1]
+    _int32(rows, heads_q, heads_k, n_pos, rot_dim)
     a = QkNormRopeArgs.from_buffer_copy(_pack_qk(
         ctypes.sizeof(QkNormRopeArgs), _dtype_code(q, "q"), _dtype_code(q_out, "q_out"), rows, heads_q, heads_k, d,
         rot_dim, ROPE_PAIRINGS[pairing], n_pos, eps, 0, q_stride, k_stride, qo_stride, ko_stride, q_ptr, k_ptr, qo_ptr,

@@ -728,6 +728,13 @@ cudaError_t launch_pair(const int8_t* a, const int8_t* b, const GemmI8Params& p,
 
 }  // namespace
 
+// Which kernel, measured on a B200 (us; N x K of the weights):
+//   1 token       one    3072 x 8192 6.3 (few 7.6), 16384 x 3072 10.2 (few 11.6)
+//   2..16         few    8 x 9216 x 3072 7.3 (flat 10.2); from 9 tokens on only up to 8192 channels, since every
+//                        warp reads the tokens again: 16 x 3072 x 3072 5.6 (flat 8.2), 16 x 16384 x 3072 17 (12.8)
+//   one wave of   flat   256 x 3072 x 3072 11.4 (pairs 13.9), 64 x 9216 x 3072 10.8 (12.5); K split while the CTAs stay
+//   tiles or less        one wave: 77 x 3072 x 4096 14.0 / 11.9 / 10.1 / 17.9 for 1 / 2 / 4 / 8 parts (24 to 192 CTAs)
+//   more tiles    pairs  512 x 9216 x 3072 15.2 (flat 25.6), 128 x 32768 x 3072 23.8 (29.9), 20 x 20480 x 3072 22.5 (21.6)
 cudaError_t launch_gemm_i8(const int8_t* a, const int8_t* b, const GemmI8Params& p, cudaStream_t s, unsigned* err,
                            std::string* emsg) {
   if (p.M == 1) return launch_one(a, b, p, s);
@@ -735,7 +742,7 @@ cudaError_t launch_gemm_i8(const int8_t* a, const int8_t* b, const GemmI8Params&
   if (p.M <= 16 && p.N <= 8192) return launch_few<2>(a, b, p, s);
   const int nt = p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
   const int64_t tiles = static_cast<int64_t>((p.N + kTileN - 1) / kTileN) * ((p.M + nt - 1) / nt);
-  if (p.M > 128 && tiles > num_sms()) {
+  if (tiles > num_sms()) {
     if (p.residual) return launch_pair<true, false>(a, b, p, s, err, emsg);
     return p.c_bf16 ? launch_pair<false, true>(a, b, p, s, err, emsg) : launch_pair<false, false>(a, b, p, s, err, emsg);
   }

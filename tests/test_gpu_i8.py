@@ -92,7 +92,7 @@ def test_quantize_every_ratio_of_bf16_values(e):
     the rule that BF16 rows are rounded without a check holds for all of them."""
     sig = torch.arange(128, 256, dtype=torch.float64, device="cuda")
     amax = sig[:, None] * 2.0 ** e
-    others = (sig[None, :] * 2.0 ** -torch.arange(0, 11, dtype=torch.float64, device="cuda")[:, None]).reshape(1, -1) * 2.0 ** e
+    others = torch.cat([sig * 2.0 ** (e - i) for i in range(11)])[None, :]
     x = torch.where(others <= amax, others, torch.zeros_like(others))
     x = torch.cat([amax, x, -x, torch.zeros(128, 15, dtype=torch.float64, device="cuda")], dim=1)
     xb = x.to(torch.bfloat16)
@@ -231,7 +231,8 @@ def check_gemm(c, a, sa, b, sb, bias, gate, res, rows=None):
 GEMM_SIZES = [(1, 1, 16), (1, 128, 64), (1, 9216, 3072), (2, 7, 48), (15, 96, 128), (16, 129, 144), (17, 127, 256),
               (33, 300, 704), (64, 704, 256), (65, 257, 1040), (77, 3072, 4096), (128, 384, 8192), (129, 131, 272),
               (255, 513, 320), (256, 256, 640), (257, 255, 3072), (300, 1000, 4096), (513, 704, 256), (1024, 768, 3072),
-              (2304, 3072, 1024), (4429, 1024, 256), (3, 2, 65536)]
+              (2304, 3072, 1024), (4429, 1024, 256), (3, 2, 65536), (9, 8200, 64), (16, 8192, 80),
+              (20, 20000, 256), (100, 19001, 128)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM_SIZES)
@@ -305,6 +306,20 @@ def test_gemm_is_the_same_on_two_streams_at_once():
             got.append((moss.op_gemm_i8(*two[:4], bias=two[4]), w2))
     torch.cuda.synchronize()
     assert all(torch.equal(g, w) for g, w in got)
+
+
+def test_a_stream_given_by_name_or_handle():
+    """The call runs on it, and its new tensors come from its pool: a long kernel before it on the current
+    stream holds nothing up and no memory of that stream is taken."""
+    a, sa, b, sb, bias, *_ = gemm_case(75, 40, 704, 512, True, False)
+    x = randn(76, 40, 512)
+    want = moss.op_gemm_i8(a, sa, b, sb, bias=bias), moss.op_quantize_i8(x)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for given in (s, s.cuda_stream):
+        got = moss.op_gemm_i8(a, sa, b, sb, bias=bias, stream=given), moss.op_quantize_i8(x, stream=given)
+        s.synchronize()
+        assert torch.equal(got[0], want[0]) and all(torch.equal(g, w) for g, w in zip(got[1], want[1]))
 
 
 # ------------------------------------------------------------------------------ query/key norm and rotation
