@@ -22,6 +22,7 @@
 
 #include "../../include/moss_dit.h"
 #include "internal.h"
+#include "ops_i8.h"
 
 namespace moss {
 

@@ -5,6 +5,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "ops_i8.h"
 
 namespace moss {
 
@@ -431,12 +432,19 @@ cudaError_t launch_mod_gemv(const bf16* W, const bf16* bias, const float* sc, fl
   return cudaGetLastError();
 }
 
-cudaError_t launch_rope_table(float2* table, int grid_h, int grid_w, int n_txt, cudaStream_t s, bool pair_major) {
+static cudaError_t launch_rope_table_as(float2* table, int grid_h, int grid_w, int n_txt, bool pair_major, cudaStream_t s) {
   const int64_t n = static_cast<int64_t>(grid_h * grid_w + n_txt) * 64;
   if (n <= 0) return cudaSuccess;
-  rope_table_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(table, grid_h, grid_w, n_txt,
-                                                                             pair_major);
+  rope_table_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(table, grid_h, grid_w, n_txt, pair_major);
   return cudaGetLastError();
+}
+
+cudaError_t launch_rope_table(float2* table, int grid_h, int grid_w, int n_txt, cudaStream_t s) {
+  return launch_rope_table_as(table, grid_h, grid_w, n_txt, true, s);
+}
+
+cudaError_t launch_rope_table_tokens(float2* table, int grid_h, int grid_w, int n_txt, cudaStream_t s) {
+  return launch_rope_table_as(table, grid_h, grid_w, n_txt, false, s);
 }
 
 cudaError_t launch_patchify(const float* latent, bf16* tokens, int h8, int w8, cudaStream_t s) {

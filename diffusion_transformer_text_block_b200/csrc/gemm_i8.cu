@@ -16,8 +16,8 @@
 //   warp 0      TMA producer: 128 x 128 bytes of B and NT x 128 bytes of A per slot (128-byte swizzle)
 //   warp 1      MMA issuer, four 32-deep steps a slot
 //   warps 2..9  epilogue (two per TMEM lane quadrant, each half of the tokens)
-#include "common.cuh"
-#include "internal.h"
+#include "i8.cuh"
+#include "ops_i8.h"
 
 namespace moss {
 

@@ -4,7 +4,7 @@
 #include <cstring>
 
 #include "../../include/moss_dit.h"
-#include "internal.h"
+#include "ops_i8.h"
 
 using namespace moss;
 
@@ -217,8 +217,8 @@ int moss_op_rope_table(float* table, int grid_h, int grid_w, int n_txt, void* st
   if (n == 0) return MOSS_OK;
   if (!table || !aligned(table, 16)) return invalid("table must not be NULL and must be 16-byte aligned");
   count_launches(1);
-  return cuda_status(launch_rope_table(reinterpret_cast<float2*>(table), grid_h, grid_w, n_txt,
-                                       static_cast<cudaStream_t>(stream), false), "rope_table", "");
+  return cuda_status(launch_rope_table_tokens(reinterpret_cast<float2*>(table), grid_h, grid_w, n_txt,
+                                              static_cast<cudaStream_t>(stream)), "rope_table", "");
 }
 
 }  // extern "C"

@@ -13,8 +13,8 @@
 // its heads, so a lane reads its gains and angles once and folds them into 16 coefficients:
 // (g_a cos, -g_b sin, g_a sin, g_b cos) per pair.  The first and the second elements of the pairs are
 // kept apart, so that all the arithmetic goes two pairs an instruction.
-#include "common.cuh"
-#include "internal.h"
+#include "i8.cuh"
+#include "ops_i8.h"
 
 namespace moss {
 

@@ -19,8 +19,8 @@
 //   rounded up, and for A = 254, where inv is a power of two and every product exact.
 //   So q equals the definition for every finite BF16 or FP32 row.  LayerNorm and SwiGLU rows carry
 //   FP32 errors of their own, larger than that of the product, and are rounded without a check.
-#include "common.cuh"
-#include "internal.h"
+#include "i8.cuh"
+#include "ops_i8.h"
 
 namespace moss {
 
