@@ -301,15 +301,15 @@ def _placed(t, dev, dtype, name):
 
 
 def _arg(t, dev, dtype, shape, name):
-    """Address of a contiguous tensor of this type and shape on the current device; None stays None."""
+    """Address of a contiguous tensor of this type (None: any) and shape on the current device; None stays None."""
     if t is None:
         return None
+    if t.shape == shape and (t.dtype is dtype or dtype is None) and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     _placed(t, dev, dtype, name)
     if t.shape != shape:
         raise MossError(1, f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise MossError(1, f"{name} must be contiguous")
-    return t.data_ptr()
+    raise MossError(1, f"{name} must be contiguous")
 
 
 def _dtype_code(t, name):
