@@ -8,14 +8,36 @@
 // FP32 (below 2^24 it is exact), and the rest is FP32 with one rounding to BF16 at the end where C
 // is BF16.
 //
-// `gemm_i8_flat_kernel`: one CTA per tile of 128 output channels and NT tokens.  The weights are the
-// 128-row operand of tcgen05.mma (kind::i8, 128 x NT x 32), so few tokens make a narrow tile and not
-// an empty one, and a thread of the epilogue holds one channel: a warp stores 32 neighbouring
-// channels of a token.  The K axis of a tile is split over the CTAs of a cluster; their partial
-// sums meet in shared memory of the cluster (integers: the order does not matter).
+// The weights are the wide operand in every kernel: few tokens then make a narrow tile and not an
+// empty one, a thread of an epilogue holds one channel (its scale, bias and gate in registers), and a
+// warp stores 32 neighbouring channels of a token (with a row a thread the epilogue of the CTA pairs
+// was as long as their products: 196 us against 179 for 9216 x 9216 x 3072).
+//
+// `gemm_i8_one_kernel` (1 token) and `gemm_i8_few_kernel` (2..16): bound by the weights' bytes.  No
+// tile, no barrier before the first load: warps read their channels with 16-byte loads straight into
+// dp4a or mma.sync (the legacy tensor path, which at this rate of bytes is nowhere near its limit;
+// tcgen05 would first have to bring the weights through shared memory).  One token through 9216 x 3072
+// 7.3 us, 3.9 TB/s of weights; the launch and the first loads' latency are 2.5 us of that.
+//
+// `gemm_i8_flat_kernel` (a wave of tiles or less): one CTA per tile of 128 output channels and NT tokens
+// (tcgen05.mma kind::i8, 128 x NT x 32), the K axis split over the CTAs of a cluster, whose partial
+// sums meet in shared memory of the cluster (integers: the order does not matter).  Bound by latencies:
+// of 9.8 us for 77 tokens x 3072 x 4096 the first slot is full after 2.1, the weights have streamed
+// after 4.5, the sums have met after 6 (clocks inside the kernel).
 //   warp 0      TMA producer: 128 x 128 bytes of B and NT x 128 bytes of A per slot (128-byte swizzle)
 //   warp 1      MMA issuer, four 32-deep steps a slot
 //   warps 2..9  epilogue (two per TMEM lane quadrant, each half of the tokens)
+//
+// `gemm_i8_pair_kernel` (more tiles): persistent CTA pairs, 256 channels x 256 tokens a pair
+// (tcgen05.mma.cta_group::2, 256 x 256 x 32) into one of two accumulators, seven 32 KB slots a CTA, the
+// epilogue of a tile under the products of the next.  Bound by the tensor pipe and, in long runs, by the
+// power cap: 9216 x 9216 x 3072 167 us = 3.1 PTOP/s, 8192^3 3.3 PTOP/s, 1.8 to 2.0 times the measured
+// BF16 rate.  (256 x 128 tiles ran at half that rate; two pairs sharing a tile's K gained 6 to 19 % below
+// 32 tiles and lost as much above.)
+//   warp 0      TMA producer, in both CTAs, counted on the even CTA's barriers
+//   warp 1      MMA issuer, even CTA only
+//   warps 2..9  epilogue, in both CTAs
+//   warp 10     even CTA: waits for the loads and hands them to warp 1 by named barriers
 #include "i8.cuh"
 #include "ops_i8.h"
 
@@ -480,9 +502,9 @@ cudaError_t launch_one(const int8_t* a, const int8_t* b, const GemmI8Params& p, 
 }
 
 // ------------------------------------------------------------------------ CTA pairs
-constexpr int kPairThreads = 320;    // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
+constexpr int kPairThreads = 352;    // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue, warp 10 hands the loads on
 
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 7;
 constexpr int kPairOpBytes = 128 * kBK;                 // one operand's rows of one CTA in a slot
 constexpr int kPairStageBytes = 2 * kPairOpBytes;       // 32 KB
 constexpr int kPairSmemBytes = kPairStages * kPairStageBytes + 1024 + 256;
@@ -607,44 +629,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (leader) drain_loads<kPairStages>(full, armed);
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
+      // The warp learns of a filled slot by a named barrier, from warp 10: a poll of an mbarrier behind
+      // queued MMAs holds up the next ones (171.8 us for 9216 x 9216 x 3072, 181.9 with polls here).  It
+      // joins every slot's barrier also after a failed wait, so that the arrivals always find it.
       constexpr uint32_t kIdesc = idesc_i8(256, 256);
       int stage = 0;
-      uint32_t phase = 0;
       bool ok = true;
       int it = 0;
-      for (int tile = pair; tile < num_tiles && ok; tile += num_pairs, ++it) {
+      for (int tile = pair; tile < num_tiles; tile += num_pairs, ++it) {
         const int acc = it & 1;
-        if (!mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1, err, kErrGemmI8Mma, abort_flag)) break;
+        if (lane == 0 && ok) ok = mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1, err, kErrGemmI8Mma, abort_flag);
+        __syncwarp();
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
         for (int kb = 0; kb < num_kb; ++kb) {
-          if (!mbar_wait(&full[stage], phase, err, kErrGemmI8Mma, abort_flag)) {
-            ok = false;
-            break;
-          }
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + stage) : "memory");
           tc_fence_after();
-          const uint32_t w0 = smem_u32(sW + stage * kPairOpBytes);
-          const uint32_t x0 = smem_u32(sX + stage * kPairOpBytes);
+          if (lane == 0 && ok) {
+            const uint32_t w0 = smem_u32(sW + stage * kPairOpBytes);
+            const uint32_t x0 = smem_u32(sX + stage * kPairOpBytes);
 #pragma unroll
-          for (int k = 0; k < kBK / 32; ++k)
-            mma_i8_ss_pair(d_tmem, sdesc_sw128(w0 + k * 32, 16, 1024), sdesc_sw128(x0 + k * 32, 16, 1024), kIdesc,
-                           (kb | k) != 0 ? 1u : 0u);
-          tc_commit_pair_both(&empty[stage], 0x3);  // the slot in both CTAs
+            for (int k = 0; k < kBK / 32; ++k)
+              mma_i8_ss_pair(d_tmem, sdesc_sw128(w0 + k * 32, 16, 1024), sdesc_sw128(x0 + k * 32, 16, 1024), kIdesc,
+                             (kb | k) != 0 ? 1u : 0u);
+            tc_commit_pair_both(&empty[stage], 0x3);  // the slot in both CTAs
+          }
+          __syncwarp();
+          if (++stage == kPairStages) stage = 0;
+        }
+        if (lane == 0 && ok) tc_commit_pair_both(&tfull[acc], 0x3);  // both CTAs' epilogues
+      }
+      // Every MMA issued by this thread has completed once `drain` flips: only then may
+      // either CTA release its TMEM, on the normal path and after an abort alike.
+      if (lane == 0) {
+        tc_commit_pair(drain);
+        const uint32_t a = smem_u32(drain);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp == 10) {
+    if (leader) {
+      // A wait that gives up is recorded and raises the abort flag; the slot is announced all the same and
+      // the kernel runs to its end on what the slots hold.
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int tile = pair; tile < num_tiles; tile += num_pairs)
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (lane == 0) mbar_wait(&full[stage], phase, err, kErrGemmI8Mma, abort_flag);
+          __syncwarp();
+          asm volatile("bar.arrive %0, 64;" ::"r"(1 + stage) : "memory");
           if (++stage == kPairStages) {
             stage = 0;
             phase ^= 1;
           }
         }
-        if (ok) tc_commit_pair_both(&tfull[acc], 0x3);  // both CTAs' epilogues
-      }
-      // Every MMA issued by this thread has completed once `drain` flips: only then may
-      // either CTA release its TMEM, on the normal path and after an abort alike.
-      tc_commit_pair(drain);
-      const uint32_t a = smem_u32(drain);
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
-      }
     }
   } else {
     const int quad = warp & 3;          // TMEM lane quadrant this warp may access
