@@ -11,14 +11,14 @@
 // Rounding.  Adding 1.5 * 2^23 to h * inv, inv = fl(127 / amax), in one FMA rounds the exact product
 // to the nearest integer, half to even, and leaves it in the sum's low byte.  h * inv is off
 // 127 h / amax by at most 127 * 2^-24 = 7.6e-6.
-//   FP32 rows: the distance |t - q| of a unit's 8 elements is compared once with 1/2 - 1.6e-5, and an
-//   element closer to a border is settled by an exact comparison in FP64.
+//   FP32 rows, and the LayerNorm's and SwiGLU's: the distance |t - q| of a unit's 8 elements is
+//   compared once with 1/2 - 1.6e-5, and an element closer to a border is settled by an exact
+//   comparison in FP64 (3 % of the SwiGLU kernel's time).
 //   BF16 rows need no such check.  With 8-bit significands X of h and A of amax, 127 h / amax is
 //   either a half-integer or, relatively, at least 1 / (254 * 255) away from one, far above FP32's
 //   error.  It is a half-integer only for h = amax / 2 (63.5), which goes to 64 because inv is
 //   rounded up, and for A = 254, where inv is a power of two and every product exact.
-//   So q equals the definition for every finite BF16 or FP32 row.  LayerNorm and SwiGLU rows carry
-//   FP32 errors of their own, larger than that of the product, and are rounded without a check.
+//   So q equals the definition for every finite row of h, h being in FP32.
 #include "i8.cuh"
 #include "ops_i8.h"
 
@@ -268,12 +268,12 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks(SRC, VPL))
         const float2 s = __ffma2_rn(v[i][e], both(inv), both(kRoundMagic));
         r[2 * e] = s.x;
         r[2 * e + 1] = s.y;
-        if constexpr (SRC == kRowF32) {
+        if constexpr (SRC != kRowBf16) {
           const float2 d = __ffma2_rn(v[i][e], both(inv), __ffma2_rn(s, both(-1.0f), both(kRoundMagic)));
           far = fmaxf(fmaxf(far, fabsf(d.x)), fabsf(d.y));
         }
       }
-      if (SRC == kRowF32 && far > kBorder) {
+      if (SRC != kRowBf16 && far > kBorder) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           r[2 * e] = settle(v[i][e].x, amax, inv, r[2 * e]);
