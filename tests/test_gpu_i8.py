@@ -103,6 +103,25 @@ def test_quantize_every_ratio_of_bf16_values(e):
     check_scale(scale, ref_scale)
 
 
+@pytest.mark.parametrize("dim", [256, 768, 1024, 1536, 2048, 3072, 4096, 6144, 8192, 12288, 16384])
+@pytest.mark.parametrize("rows", [2, 200, 700, 1300])
+def test_every_team_size(rows, dim):
+    """Rows that fill their lanes exactly, with 1, 2, 4 and 8 warps a row as the number of rows asks for: all
+    four sources, the integers exact for BF16 and FP32 rows and within FP32's error of h for the others."""
+    x = randn(11, rows, dim)
+    for v in (x, x.bfloat16()):
+        q, scale = moss.op_quantize_i8(v)
+        ref, ref_scale = quantized(v.double())
+        assert torch.equal(q.double(), ref)
+        check_scale(scale, ref_scale)
+    shift, mscale = randn(12, dim, scale=0.1), randn(13, dim, scale=0.1)
+    q, qs = moss.op_ln_modulate_i8(x, shift, mscale)
+    check_rows_of(q, qs, *layer_norm_reference(x, shift, mscale))
+    gu = randn(14, rows, 2 * dim, scale=2.0).bfloat16()
+    q, qs = moss.op_swiglu_i8(gu)
+    check_rows_of(q, qs, *swiglu_reference(gu))
+
+
 def test_quantize_extremes():
     """Subnormal rows, the largest finite values, one element set, and rows that are not finite."""
     tiny, big = 2.0 ** -149, float(np.finfo(np.float32).max)
@@ -156,37 +175,46 @@ def check_rows_of(q, scale, h, err):
     assert ((q.double() * scale.double()[:, None] - h).abs() <= bound).all()
 
 
-@pytest.mark.parametrize("rows,dim", [(1, 128), (37, 256), (333, 3072), (5, 8192), (2, 20000), (1, 16)])
-def test_ln_modulate_i8(rows, dim):
-    """FP32 errors of a row: a sum of at most 16 x 8 terms a lane, 5 shuffles and 8 warps is off by
+def layer_norm_reference(x, shift, scale):
+    """(h, bound on FP32's error).  A sum of at most 16 x 8 terms a lane, 5 shuffles and 8 warps is off by
     d u sum|x| with d = 141; the centred value x - mean by d u mean|x| + u|x - mean|; the variance, a sum
     of squares of those, relatively by (d + 4) u + 2 d u mean|x| / std (first order), 1/std by half of that and
     rsqrtf's 2 ulp (4 u); (1 + scale), the product and the sum add 4 u."""
-    x = randn(7, rows, dim, scale=3.0) + 0.5
-    shift, scale = randn(8, dim, scale=0.1), randn(9, dim, scale=0.1)
-    q, qs = moss.op_ln_modulate_i8(x, shift, scale)
     xd, m = x.double(), 1 + scale.double()
     mean = xd.mean(dim=1, keepdim=True)
     std = torch.sqrt(((xd - mean) ** 2).mean(dim=1, keepdim=True) + 1e-6)
     n = (xd - mean) / std
     h = n * m + shift.double()
-    ref = torch.from_numpy(o.ln_modulate(xd.cpu().numpy(), shift.double().cpu().numpy(), scale.double().cpu().numpy()))
-    assert (h.cpu() - ref).abs().max() <= 1e-12
     d, mabs = 141, xd.abs().mean(dim=1, keepdim=True)
     err = m.abs() * ((d * U * mabs / std) + n.abs() * U * (1 + (d + 4) / 2 + d * mabs / std + 4 + 4)) + 2 * U * h.abs()
-    check_rows_of(q, qs, h, 1.01 * err)
+    return h, 1.01 * err
+
+
+def swiglu_reference(gu):
+    """(h, bound on FP32's error).  h = g / (1 + e^-g) u: __expf is within 2 + 1.173|g| ulp (2 u each), which the
+    sum weakens; the sum, the approximate division (2 ulp) and the product add 1 + 4 + 1 u."""
+    g, u = gu.double().chunk(2, dim=1)
+    h = g * torch.sigmoid(g) * u
+    return h, 1.01 * h.abs() * U * (2 * (2 + 1.173 * g.abs()) + 8)
+
+
+@pytest.mark.parametrize("rows,dim", [(1, 128), (37, 256), (333, 3072), (5, 8192), (2, 20000), (1, 16)])
+def test_ln_modulate_i8(rows, dim):
+    x = randn(7, rows, dim, scale=3.0) + 0.5
+    shift, scale = randn(8, dim, scale=0.1), randn(9, dim, scale=0.1)
+    q, qs = moss.op_ln_modulate_i8(x, shift, scale)
+    h, err = layer_norm_reference(x, shift, scale)
+    ref = torch.from_numpy(o.ln_modulate(x.double().cpu().numpy(), shift.double().cpu().numpy(), scale.double().cpu().numpy()))
+    assert (h.cpu() - ref).abs().max() <= 1e-12
+    check_rows_of(q, qs, h, err)
 
 
 @pytest.mark.parametrize("rows,dim", [(1, 64), (37, 704), (333, 8192), (2, 32768), (3, 16)])
 def test_swiglu_i8(rows, dim):
-    """h = g / (1 + e^-g) u: __expf is within 2 + 1.173|g| ulp (2 u each), which the sum weakens; the sum, the
-    approximate division (2 ulp) and the product add 1 + 4 + 1 u."""
     gu = randn(10, rows, 2 * dim, scale=2.0).bfloat16()
     gu[:, 0], gu[:, 1], gu[:, dim:dim + 2] = -40.0, 30.0, 0.5
     q, qs = moss.op_swiglu_i8(gu)
-    g, u = gu.double().chunk(2, dim=1)
-    h = g * torch.sigmoid(g) * u
-    check_rows_of(q, qs, h, 1.01 * h.abs() * U * (2 * (2 + 1.173 * g.abs()) + 8))
+    check_rows_of(q, qs, *swiglu_reference(gu))
 
 
 def test_swiglu_limits():
@@ -232,7 +260,8 @@ GEMM_SIZES = [(1, 1, 16), (1, 128, 64), (1, 9216, 3072), (2, 7, 48), (15, 96, 12
               (33, 300, 704), (64, 704, 256), (65, 257, 1040), (77, 3072, 4096), (128, 384, 8192), (129, 131, 272),
               (255, 513, 320), (256, 256, 640), (257, 255, 3072), (300, 1000, 4096), (513, 704, 256), (1024, 768, 3072),
               (2304, 3072, 1024), (4429, 1024, 256), (3, 2, 65536), (9, 8200, 64), (16, 8192, 80),
-              (20, 20000, 256), (100, 19001, 128)]
+              (20, 20000, 256), (100, 19001, 128), (20001, 300, 16),
+              (50001, 1, 64), (17, 1, 16), (8, 5, 8192), (11, 33, 4096), (16, 40, 16384)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM_SIZES)
@@ -395,6 +424,22 @@ def test_qk_in_place_leaves_the_values_and_matches_out_of_place():
     moss.op_qk_norm_rope(q, k, gain, gain, rope, q_out=q, k_out=k)
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
     assert torch.equal(qkv[:, 2 * H * d:], start[:, 2 * H * d:]) and torch.equal(qkv[rows], start[rows])
+
+
+@pytest.mark.parametrize("pairing", ["adjacent", "halves"])
+def test_qk_from_and_to_buffers_of_other_strides(pairing):
+    """q and k in tensors of their own, written into the columns of a wider buffer."""
+    rows, hq, hk, d = 45, 6, 2, 64
+    q, k = randn(86, rows + 3, hq + 1, d)[:rows, :hq], randn(87, rows, hk, d)
+    gq, gk, rope = 1 + randn(88, d, scale=0.1), 1 + randn(89, d, scale=0.1), angles(90, rows, d)
+    wide = torch.full((rows, 3 * d + (hq + hk) * d + d), 4.0, device="cuda", dtype=torch.bfloat16)
+    qo = wide[:, 2 * d:(2 + hq) * d].view(rows, hq, d)
+    ko = wide[:, (3 + hq) * d:(3 + hq + hk) * d].view(rows, hk, d)
+    moss.op_qk_norm_rope(q, k, gq, gk, rope, pairing=pairing, q_out=qo, k_out=ko)
+    at = torch.arange(rows, device="cuda")
+    check_qk(qo, q, gq, rope, at, pairing, 1e-6)
+    check_qk(ko, k, gk, rope, at, pairing, 1e-6)
+    assert (wide[:, :2 * d] == 4).all() and (wide[:, (2 + hq) * d:(3 + hq) * d] == 4).all() and (wide[:, -d:] == 4).all()
 
 
 def test_qk_without_gains_and_with_rows_that_are_not_finite():
