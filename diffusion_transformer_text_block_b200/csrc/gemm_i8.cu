@@ -97,27 +97,28 @@ __device__ __forceinline__ void store_value(const GemmI8Params& p, const I8Chann
     static_cast<float*>(p.c)[at] = v;
 }
 
-// The same for 16 tokens from m on, `count` of them inside C: every load before the first store.
-__device__ __forceinline__ void store_values16(const GemmI8Params& p, const I8Channel& ch, const uint32_t (&acc)[16],
-                                               const float* scales, int m, int count, int n) {
+// The same for B tokens from m on, `count` of them inside C: every load before the first store.
+template <int B>
+__device__ __forceinline__ void store_values(const GemmI8Params& p, const I8Channel& ch, const uint32_t (&acc)[B],
+                                             const float* scales, int m, int count, int n) {
   const int64_t at = static_cast<int64_t>(m) * p.N + n;
-  float v[16];
+  float v[B];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = fmaf(__int2float_rn(static_cast<int>(acc[i])) * scales[i], ch.scale, ch.bias);
+  for (int i = 0; i < B; ++i) v[i] = fmaf(__int2float_rn(static_cast<int>(acc[i])) * scales[i], ch.scale, ch.bias);
   if (p.residual) {
-    float r[16];
+    float r[B];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = i < count ? p.residual[at + static_cast<int64_t>(i) * p.N] : 0.f;
+    for (int i = 0; i < B; ++i) r[i] = i < count ? p.residual[at + static_cast<int64_t>(i) * p.N] : 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = fmaf(ch.gate, v[i], r[i]);
+    for (int i = 0; i < B; ++i) v[i] = fmaf(ch.gate, v[i], r[i]);
   }
   if (p.c_bf16) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < B; ++i)
       if (i < count) static_cast<bf16*>(p.c)[at + static_cast<int64_t>(i) * p.N] = __float2bfloat16_rn(v[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < B; ++i)
       if (i < count) static_cast<float*>(p.c)[at + static_cast<int64_t>(i) * p.N] = v[i];
   }
 }
@@ -252,12 +253,13 @@ __global__ void __launch_bounds__(kFlatThreads, 1)
       for (int c = half * 16; c < NT && m0 + c < p.M; c += 32) {
         uint32_t v[16];
         tmem_ld16(tb + c, v);
-        if (n < p.N) store_values16(p, ch, v, scales + c, m0 + c, min(16, p.M - m0 - c), n);
+        if (n < p.N) store_values<16>(p, ch, v, scales + c, m0 + c, min(16, p.M - m0 - c), n);
       }
     }
   } else {
     // split is a power of two: CTA r finishes the tile's tokens [r share, (r + 1) share), and every CTA
     // writes its partial sums of them to r's shared memory, [CTA][token][channel].
+    static_assert(NT / kMaxSplit >= 4 && NT % 16 == 0, "four tokens have one owner");
     const int shift = __popc(NT / split - 1), share = 1 << shift;
     const int tokens = min(NT, p.M - m0);
     __syncwarp();
@@ -269,27 +271,31 @@ __global__ void __launch_bounds__(kFlatThreads, 1)
         uint32_t v[16];
         tmem_ld16(tb + c, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (c + i < tokens)
-            st_cluster_u32(mapa_shared(mine + ((c + i) & (share - 1)) * kTileN * 4, (c + i) >> shift), v[i]);
+        for (int i = 0; i < 16; i += 4) {  // four tokens have one owner: share >= 4
+          const uint32_t to = mapa_shared(mine + ((c + i) & (share - 1)) * kTileN * 4, (c + i) >> shift);
+          if (c + i < tokens) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) st_cluster_u32(to + j * kTileN * 4, v[i + j]);
+          }
+        }
       }
     }
     __syncwarp();
     cluster_sync();
     if (epi && ok && n < p.N) {
+      // Eight tokens a round: the code runs once or twice, and a longer body waits for its own instructions
+      // (16 a round: 8.2 us instead of 7.4 for 24 x 3072 x 3072).
+      constexpr int kB = 8;
       const int c0 = rank * share, count = min(share, tokens - c0);
-      const int i1 = half ? count : min(count, (share + 1) / 2);
 #pragma unroll 1
-      for (int i0 = half ? (share + 1) / 2 : 0; i0 < i1; i0 += 16) {
-        uint32_t sum[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum[i] = 0;
-#pragma unroll 1
+      for (int i0 = half * kB; i0 < count; i0 += 2 * kB) {
+        uint32_t sum[kB] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 2
         for (int r = 0; r < split; ++r)
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (i0 + i < i1) sum[i] += part[(r * share + i0 + i) * kTileN + ln];
-        store_values16(p, ch, sum, scales + c0 + i0, m0 + c0 + i0, min(16, i1 - i0), n);
+          for (int i = 0; i < kB; ++i)
+            if (i0 + i < count) sum[i] += part[(r * share + i0 + i) * kTileN + ln];
+        store_values<kB>(p, ch, sum, scales + c0 + i0, m0 + c0 + i0, min(kB, count - i0), n);
       }
     }
   }
