@@ -164,6 +164,7 @@ int moss_op_qk_norm_rope(const moss_qk_norm_rope_args* a, void* stream) {
   if (a->rows < 0 || a->heads_q < 1 || a->heads_k < 0) return invalid("need rows >= 0, heads_q >= 1, heads_k >= 0");
   if (a->heads_q > 65536 || a->heads_k > 65536) return invalid("at most 65536 heads");
   if (!(a->eps >= 0.f)) return invalid("eps must be >= 0");
+  if (a->reserved != 0) return invalid("reserved must be 0");
   const int64_t ib = dtype_bytes(a->in_dtype), ob = dtype_bytes(a->out_dtype);
   const int64_t wq = static_cast<int64_t>(a->heads_q) * a->head_dim, wk = static_cast<int64_t>(a->heads_k) * a->head_dim;
   const bool has_k = a->heads_k > 0;

@@ -114,7 +114,7 @@ def test_qk_refusals():
     assert qk(struct_size=16) == ABI
     assert qk(head_dim=96) == UNSUPPORTED
     for kw in (dict(in_dtype=2), dict(out_dtype=-1), dict(pairing=2), dict(rot_dim=-8), dict(rot_dim=136), dict(rot_dim=12),
-               dict(rows=-1), dict(heads_q=0), dict(heads_k=-1), dict(heads_q=70000), dict(eps=-1.0), dict(eps=float("nan")),
+               dict(rows=-1), dict(heads_q=0), dict(heads_k=-1), dict(heads_q=70000), dict(eps=-1.0), dict(eps=float("nan")), dict(reserved=1),
                dict(q_stride=255), dict(k_stride=248), dict(q_out_stride=260), dict(k_out_stride=0),
                dict(q_stride=(1 << 40) + 8), dict(q=None), dict(k=None), dict(q_out=None), dict(k_out=None), dict(rope=None),
                dict(n_pos=0), dict(rot_dim=0, positions=BASE * 9), dict(q=BASE + 8), dict(k_out=BASE * 4 + 2),
