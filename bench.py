@@ -15,6 +15,7 @@ step); replicas only: each rank runs its own image, no collective on the data pa
 from __future__ import annotations
 
 import argparse
+import itertools
 import json
 import os
 import statistics
@@ -484,6 +485,86 @@ def run_accel(args):
     return 0
 
 
+def run_i8(args):
+    """The 8-bit operators and the query/key norm on the 1024^2 block shapes (batch 2, 4096 image + 512 text
+    tokens), each alone and as one joint block (its linear layers on 8-bit integers, attention in BF16).  The
+    calls are captured in a CUDA graph and the graph is replayed between CUDA events; inputs are larger than
+    L2, alone or with those of the calls before.  Prints one JSON line: per operator the device time and its rate, of the
+    measured HBM rate or as TOP/s."""
+    import torch
+
+    import diffusion_transformer_text_block_b200 as moss
+    from synth import FULL, make_residual, make_weights
+
+    D, F, H, N = FULL.hidden, FULL.ffn, FULL.heads, 4096 + N_TXT
+    rows = 2 * N
+    w = make_weights(FULL, 3, device="cuda", layers=1)
+    x = make_residual(2, N, D, 4, device="cuda").view(rows, D)
+    mod = [torch.randn(D, device="cuda") * 0.1 for _ in range(6)]
+    q8 = {"qkv": moss.op_quantize_i8(w["wqkv"][0]), "o": moss.op_quantize_i8(w["wo"][0]),
+          "gu": moss.op_quantize_i8(torch.cat([w["wg"][0], w["wu"][0]])), "down": moss.op_quantize_i8(w["wd"][0])}
+    rope = moss.op_rope_table(64, 64, N_TXT)
+    out = torch.empty_like(x)
+
+    def qk(qkv):
+        q, k = (qkv[:, i * D:(i + 1) * D].view(rows, H, 128) for i in (0, 1))
+        moss.op_qk_norm_rope(q, k, w["q_gain"][0], w["k_gain"][0], rope, q_out=q, k_out=k)
+
+    def block():
+        qkv = moss.op_gemm_i8(*moss.op_ln_modulate_i8(x, mod[0], mod[1]), *q8["qkv"])
+        qk(qkv)
+        o = moss.op_attention(qkv.view(2, N, 3 * D), H).view(rows, D)
+        mid = moss.op_gemm_i8(*moss.op_quantize_i8(o), *q8["o"], gate=mod[2], residual=x)
+        gu = moss.op_gemm_i8(*moss.op_ln_modulate_i8(mid, mod[3], mod[4]), *q8["gu"])
+        moss.op_gemm_i8(*moss.op_swiglu_i8(gu), *q8["down"], gate=mod[5], residual=mid, out=out)
+
+    h8 = moss.op_ln_modulate_i8(x, mod[0], mod[1])
+    qkv = moss.op_gemm_i8(*h8, *q8["qkv"])
+    gu = moss.op_gemm_i8(*h8, *q8["gu"])
+    act = moss.op_swiglu_i8(gu)
+    turns = itertools.cycle([qkv, qkv.clone(), qkv.clone()])  # together larger than L2, whichever part is read
+    runs = {  # name: (call, bytes, integer operations)
+        "ln_modulate_i8": (lambda: moss.op_ln_modulate_i8(x, mod[0], mod[1]), rows * D * 5, 0),
+        "gemm_i8_qkv": (lambda: moss.op_gemm_i8(*h8, *q8["qkv"]), 0, 2 * rows * 3 * D * D),
+        "qk_norm_rope": (lambda: qk(next(turns)), rows * 2 * D * 4, 0),
+        "quantize_i8": (lambda: moss.op_quantize_i8(next(turns)[:, 2 * D:]), rows * D * 3, 0),
+        "gemm_i8_o_residual": (lambda: moss.op_gemm_i8(*h8, *q8["o"], gate=mod[2], residual=x, out=out), 0,
+                               2 * rows * D * D),
+        "gemm_i8_gate_up": (lambda: moss.op_gemm_i8(*h8, *q8["gu"]), 0, 2 * rows * 2 * F * D),
+        "swiglu_i8": (lambda: moss.op_swiglu_i8(gu), rows * F * 5, 0),
+        "gemm_i8_down_residual": (lambda: moss.op_gemm_i8(*act, *q8["down"], gate=mod[5], residual=x, out=out), 0,
+                                  2 * rows * D * F),
+        "block": (block, 0, 0),
+    }
+    peaks = read_peaks()
+    res = {"op": "i8", "workload": f"{rows} tokens (2 branches of {N}), hidden {D}, FFN {F}", "operators": {}}
+    for name, (call, nbytes, ops) in runs.items():
+        call()
+        torch.cuda.synchronize()
+        n = max(args.steps, 8)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(n):
+                call()
+        graph.replay()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        graph.replay()
+        e1.record()
+        torch.cuda.synchronize()
+        us = e0.elapsed_time(e1) * 1e3 / n
+        del graph
+        rec = {"us": round(us, 2)}
+        if nbytes:
+            rec["hbm_frac"] = round(nbytes / (us * 1e-6) / 1e9 / peaks["hbm_gbs"], 3)
+        if ops:
+            rec["tops"] = round(ops / (us * 1e-6) / 1e12, 1)
+        res["operators"][name] = rec
+    res["device_status"] = moss.device_status(clear=True)
+    print(json.dumps(res), flush=True)
+    return 0
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -492,9 +573,9 @@ def main():
     ap.add_argument("--impl", default="ours", choices=["ours", "reference"])
     ap.add_argument("--e2e-steps", type=int, default=10)
     ap.add_argument("--no-cpu-baseline", action="store_true")
-    ap.add_argument("--op", choices=["block", "attention", "accel", "text", "c5", "cfg_euler"], default=None,
+    ap.add_argument("--op", choices=["block", "attention", "accel", "text", "c5", "cfg_euler", "i8"], default=None,
                     help="time one kernel class on the 1024^2 shapes instead of the denoising step; "
-                         "'accel' times whole 50-step images with the lossy accelerators")
+                         "'accel' times whole 50-step images with the lossy accelerators, 'i8' the 8-bit operators")
     args = ap.parse_args()
     if args.impl == "reference":
         return run_reference(args)
@@ -506,6 +587,8 @@ def main():
         return run_c5(args)
     if args.op == "cfg_euler":
         return run_cfg_euler(args)
+    if args.op == "i8":
+        return run_i8(args)
     if args.op:
         return run_op(args)
 

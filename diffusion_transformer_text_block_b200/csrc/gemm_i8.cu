@@ -711,14 +711,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (p.bias) ch.bias = __bfloat162float(p.bias[n]);
         if constexpr (RESID) ch.gate = __ldg(p.gate + n);
       }
-      if constexpr (RESID) {
-        // The warp's part of the residual (32 channels of 128 tokens, a line each) comes to L2 meanwhile.
-        const int n0 = n - lane;
-#pragma unroll
-        for (int i = 0; i < 128; i += 32)
-          if (n0 < p.N && m0 + lane + i < p.M)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.residual + static_cast<int64_t>(m0 + lane + i) * p.N + n0));
-      }
       const bool ok = mbar_wait(&tfull[acc], (it >> 1) & 1, err, kErrGemmI8Epilogue, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) break;  // warp-uniform: TMEM loads are .sync.aligned
       tc_fence_after();
