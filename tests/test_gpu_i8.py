@@ -321,6 +321,29 @@ def test_gemm_output_beyond_32_bit_offsets():
     check_gemm(c, a, sa, b, sb, None, None, None, rows=rows)
 
 
+def test_calls_from_two_threads():
+    """Two threads, a stream each, calls of different kernels: nothing is shared but what the library guards."""
+    import threading
+    cases = [gemm_case(62, 300, 704, 1024, False, False), gemm_case(72, 5, 3072, 1024, False, False)]
+    want = [moss.op_gemm_i8(*c[:4]) for c in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got[i].append(moss.op_gemm_i8(*cases[i][:4]))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in (0, 1):
+        assert len(got[i]) == 50 and all(torch.equal(g, want[i]) for g in got[i])
+
+
 def test_gemm_is_the_same_on_two_streams_at_once():
     one, two = gemm_case(60, 300, 704, 1024, False, False), gemm_case(70, 5, 3072, 1024, True, False)
     w1 = moss.op_gemm_i8(*one[:4])
@@ -345,9 +368,9 @@ def test_a_stream_given_by_name_or_handle():
     want = moss.op_gemm_i8(a, sa, b, sb, bias=bias), moss.op_quantize_i8(x)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
-    for given in (s, s.cuda_stream):
+    for given in (s, s.cuda_stream, torch.cuda.default_stream(), 0):
         got = moss.op_gemm_i8(a, sa, b, sb, bias=bias, stream=given), moss.op_quantize_i8(x, stream=given)
-        s.synchronize()
+        torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and all(torch.equal(g, w) for g, w in zip(got[1], want[1]))
 
 
