@@ -49,7 +49,8 @@ int check_rows_out(const Span& in, int8_t* q, float* scale, int rows, int dim) {
   return MOSS_OK;
 }
 
-constexpr int64_t kMaxStride = int64_t{1} << 40;  // elements; keeps byte offsets within 64 bits
+// Whether `rows` rows `stride` bytes apart lie within an address space (and their offsets within 64 bits).
+bool stride_fits(int64_t stride, int64_t rows) { return stride <= (int64_t{1} << 47) / (rows > 0 ? rows : 1); }
 
 const char* kRowsDims = "rows must be >= 0 and dim a positive multiple of 16, at most 32768";
 bool rows_dims_ok(int rows, int dim) { return rows >= 0 && dim >= 16 && dim % 16 == 0 && dim <= kMaxRowDim; }
@@ -64,7 +65,8 @@ int moss_op_quantize_i8(const void* x, int x_dtype, int64_t x_stride, int8_t* q,
   if (!known_dtype(x_dtype)) return invalid("x_dtype must be MOSS_DTYPE_F32 or MOSS_DTYPE_BF16");
   if (!rows_dims_ok(rows, dim)) return invalid(kRowsDims);
   const int64_t eb = dtype_bytes(x_dtype);
-  if (x_stride < dim || x_stride % (16 / eb) || x_stride > kMaxStride) return invalid("x_stride must be >= dim and a multiple of 16 bytes");
+  if (x_stride < dim || x_stride % (16 / eb)) return invalid("x_stride must be >= dim and a multiple of 16 bytes");
+  if (!stride_fits(x_stride, rows)) return invalid("x_stride is too long");
   if (rows == 0) return MOSS_OK;
   if (!x || !aligned(x, 16)) return invalid("x must not be NULL and must be 16-byte aligned");
   if (int rc = check_rows_out(Span(x, dim * eb, x_stride * eb, rows), q, scale, rows, dim)) return rc;
@@ -93,8 +95,8 @@ int moss_op_ln_modulate_i8(const float* x, const float* shift, const float* scal
 int moss_op_swiglu_i8(const void* gu, int64_t gu_stride, int8_t* q, float* scale, int rows, int dim, void* stream) {
   set_error(MOSS_OK, "");
   if (!rows_dims_ok(rows, dim)) return invalid(kRowsDims);
-  if (gu_stride < 2 * static_cast<int64_t>(dim) || gu_stride % 8 || gu_stride > kMaxStride)
-    return invalid("gu_stride must be >= 2 dim and a multiple of 8");
+  if (gu_stride < 2 * static_cast<int64_t>(dim) || gu_stride % 8) return invalid("gu_stride must be >= 2 dim and a multiple of 8");
+  if (!stride_fits(gu_stride, rows)) return invalid("gu_stride is too long");
   if (rows == 0) return MOSS_OK;
   if (!gu || !aligned(gu, 16)) return invalid("gu must not be NULL and must be 16-byte aligned");
   if (int rc = check_rows_out(Span(gu, 4 * static_cast<int64_t>(dim), 2 * gu_stride, rows), q, scale, rows, dim)) return rc;
@@ -111,9 +113,9 @@ int moss_op_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, cons
     return invalid("need M >= 0, N >= 1 and K a multiple of 16, 16 <= K <= 65536");
   if ((gate == nullptr) != (residual == nullptr)) return invalid("gate and residual go together");
   if (residual && c_dtype != MOSS_DTYPE_F32) return invalid("the gated residual form writes FP32");
-  const int64_t out = static_cast<int64_t>(M) * N * dtype_bytes(c_dtype);
   if (((static_cast<int64_t>(M) + 15) / 16) * ((static_cast<int64_t>(N) + 127) / 128) * 8 > 0x7fffffff)
     return invalid("M * N is too large");
+  const int64_t out = static_cast<int64_t>(M) * N * dtype_bytes(c_dtype);
   if (M == 0) return MOSS_OK;
   if (!a || !a_scale || !b || !b_scale || !c) return invalid("a, a_scale, b, b_scale and c must not be NULL");
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(c, 16) || !aligned(residual, 16))
@@ -170,7 +172,8 @@ int moss_op_qk_norm_rope(const moss_qk_norm_rope_args* a, void* stream) {
   const bool has_k = a->heads_k > 0;
   if (a->q_stride < wq || a->q_out_stride < wq || (has_k && (a->k_stride < wk || a->k_out_stride < wk)))
     return invalid("a stride is shorter than its row of heads");
-  if (a->q_stride > kMaxStride || a->q_out_stride > kMaxStride || (has_k && (a->k_stride > kMaxStride || a->k_out_stride > kMaxStride)))
+  if (!stride_fits(a->q_stride, a->rows) || !stride_fits(a->q_out_stride, a->rows) ||
+      (has_k && (!stride_fits(a->k_stride, a->rows) || !stride_fits(a->k_out_stride, a->rows))))
     return invalid("a stride is too long");
   if (a->q_stride * ib % 16 || a->q_out_stride * ob % 16 || (has_k && (a->k_stride * ib % 16 || a->k_out_stride * ob % 16)))
     return invalid("strides must be multiples of 16 bytes");

@@ -35,7 +35,7 @@ def test_quantize_refusals():
         return f(x, dt, stride, q, s, rows, dim, None)
 
     for kw in (dict(dt=2), dict(dt=-1), dict(rows=-1), dict(dim=0), dict(dim=8), dict(dim=24), dict(dim=32784, stride=32784),
-               dict(stride=63), dict(stride=68), dict(stride=66, dt=moss.DTYPE_F32), dict(stride=(1 << 40) + 8),
+               dict(stride=63), dict(stride=68), dict(stride=66, dt=moss.DTYPE_F32), dict(stride=(1 << 46) + 8), dict(stride=1 << 30, rows=1 << 20),
                dict(x=None), dict(q=None), dict(s=None), dict(x=P(BASE + 8)), dict(q=P(BASE * 2 + 8)), dict(s=P(BASE * 3 + 2)),
                dict(q=at(0)), dict(s=at(0)), dict(s=at(1)), dict(q=P(BASE + 3 * 128 + 112))):
         assert call(**kw) == INVALID, kw
@@ -81,7 +81,7 @@ def test_gemm_refusals():
                dict(sa=P(BASE * 2 + 2)), dict(bias=P(BASE * 6 + 1)), dict(gate=at(5)), dict(resid=at(5), dt=f32),
                dict(gate=at(5), resid=at(6)), dict(gate=at(5), resid=P(BASE * 7 + 4), dt=f32), dict(c=at(0)), dict(c=at(1)),
                dict(c=at(2)), dict(c=at(3)), dict(bias=at(4)), dict(gate=at(4), resid=at(6), dt=f32),
-               dict(gate=at(5), resid=P(BASE * 5 + 16), dt=f32), dict(M=1 << 30, N=1 << 20)):
+               dict(gate=at(5), resid=P(BASE * 5 + 16), dt=f32), dict(M=1 << 30, N=1 << 20), dict(M=(1 << 31) - 1, N=(1 << 31) - 1)):
         assert call(**kw) == INVALID, kw
     assert call(a=None, sa=None, b=None, sb=None, c=None, M=0) == 0
 
@@ -116,7 +116,7 @@ def test_qk_refusals():
     for kw in (dict(in_dtype=2), dict(out_dtype=-1), dict(pairing=2), dict(rot_dim=-8), dict(rot_dim=136), dict(rot_dim=12),
                dict(rows=-1), dict(heads_q=0), dict(heads_k=-1), dict(heads_q=70000), dict(eps=-1.0), dict(eps=float("nan")), dict(reserved=1),
                dict(q_stride=255), dict(k_stride=248), dict(q_out_stride=260), dict(k_out_stride=0),
-               dict(q_stride=(1 << 40) + 8), dict(q=None), dict(k=None), dict(q_out=None), dict(k_out=None), dict(rope=None),
+               dict(q_stride=(1 << 46) + 8), dict(k_out_stride=1 << 30, rows=1 << 20), dict(q=None), dict(k=None), dict(q_out=None), dict(k_out=None), dict(rope=None),
                dict(n_pos=0), dict(rot_dim=0, positions=BASE * 9), dict(q=BASE + 8), dict(k_out=BASE * 4 + 2),
                dict(q_gain=BASE * 8 + 4), dict(positions=BASE * 9 + 2), dict(rope=BASE * 5 + 8),
                dict(q_out=BASE + 16), dict(k_out=BASE * 2 + 512),                                # shifted onto their input
