@@ -330,10 +330,11 @@ def _new(ref, shape, dtype, stream):
         return ref.new_empty(shape, dtype=dtype)
 
 
-def _int32(*sizes):
-    """The C calls take sizes as 32-bit integers."""
-    if max(sizes) > 0x7fffffff:
-        raise MossError(1, "a size does not fit 32 bits")
+_INT32_MAX = 0x7fffffff  # the C calls take sizes as 32-bit integers
+
+
+def _too_large():
+    raise MossError(1, "a size does not fit 32 bits")
 
 
 def _rows_of(t, name):
@@ -341,7 +342,8 @@ def _rows_of(t, name):
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise MossError(1, f"{name} must be [rows, dim] with contiguous rows")
     rows, width = t.shape
-    _int32(rows, width)
+    if rows > _INT32_MAX or width > _INT32_MAX:
+        _too_large()
     return rows, width, t.stride(0) if rows > 1 else width
 
 
@@ -363,7 +365,8 @@ def op_ln_modulate_i8(x, shift, scale, stream=None):
     """LN(x) (1 + scale) + shift of FP32 x [rows, dim], made 8-bit by rows: (q int8, q_scale FP32 [rows])."""
     torch, dev = _begin(x, "x")
     rows, dim = x.shape
-    _int32(rows, dim)
+    if rows > _INT32_MAX or dim > _INT32_MAX:
+        _too_large()
     f = torch.float32
     q = _new(x, (rows, dim), torch.int8, stream)
     q_scale = _new(x, rows, f, stream)
@@ -398,7 +401,8 @@ def op_gemm_i8(a, a_scale, b, b_scale, bias=None, gate=None, residual=None, out_
         raise MossError(1, "a must be [M, K] and b [N, K]")
     M, K = a.shape
     N = b.shape[0]
-    _int32(M, N, K)
+    if M > _INT32_MAX or N > _INT32_MAX or K > _INT32_MAX:
+        _too_large()
     f, i8 = torch.float32, torch.int8
     if out is None:
         out = _new(a, (M, N), out_dtype or (f if residual is not None else torch.bfloat16), stream)
@@ -406,8 +410,9 @@ def op_gemm_i8(a, a_scale, b, b_scale, bias=None, gate=None, residual=None, out_
         raise MossError(1, f"out is {out.dtype}, not {out_dtype}")
     _check(lib().moss_op_gemm_i8(
         _arg(a, dev, i8, (M, K), "a"), _arg(a_scale, dev, f, (M,), "a_scale"), _arg(b, dev, i8, (N, K), "b"),
-        _arg(b_scale, dev, f, (N,), "b_scale"), _arg(bias, dev, torch.bfloat16, (N,), "bias"),
-        _arg(gate, dev, f, (N,), "gate"), _arg(residual, dev, f, (M, N), "residual"),
+        _arg(b_scale, dev, f, (N,), "b_scale"), bias if bias is None else _arg(bias, dev, torch.bfloat16, (N,), "bias"),
+        gate if gate is None else _arg(gate, dev, f, (N,), "gate"),
+        residual if residual is None else _arg(residual, dev, f, (M, N), "residual"),
         _arg(out, dev, None, (M, N), "out"), _dtype_code(out, "out"), M, N, K, _raw_stream(stream, dev)))
     return out
 
@@ -467,7 +472,8 @@ def op_qk_norm_rope(q, k, q_gain, k_gain, rope, positions=None, pairing="adjacen
             raise MossError(1, "rope must be [n_pos, rot_dim/2, 2]")
         rope_ptr = _arg(rope, dev, f, shape, "rope")
         n_pos, rot_dim = shape[0], 2 * shape[1]
-    _int32(rows, heads_q, heads_k, n_pos, rot_dim)
+    if max(rows, heads_q, heads_k, n_pos, rot_dim) > _INT32_MAX:
+        _too_large()
     a = QkNormRopeArgs.from_buffer_copy(_pack_qk(
         ctypes.sizeof(QkNormRopeArgs), _dtype_code(q, "q"), _dtype_code(q_out, "q_out"), rows, heads_q, heads_k, d,
         rot_dim, ROPE_PAIRINGS[pairing], n_pos, eps, 0, q_stride, k_stride, qo_stride, ko_stride, q_ptr, k_ptr, qo_ptr,
