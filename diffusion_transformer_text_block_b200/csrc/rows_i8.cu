@@ -51,6 +51,29 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4& p, float2 (&v)[4]) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
+// SiLU(g) u for 8 elements.  1 + e^-g passes 2^126, where the fast division gives 0, below g = -87.3, and FP32's
+// range below -88.7, while SiLU(g) is a normal number down to -92 and one that a large u brings back further
+// still.  Below -87, 1 + e^-g is e^-g in FP32 and SiLU(g) u = u e^(g/2) g e^(g/2), whose running product is never
+// smaller than the result.  A unit takes that path for a gate whose BF16 pattern lies above that of -87 (0xc2ae):
+// one comparison for 8 elements (9216 x 8192: 59.7 us with it, 60.8 without, in turn).
+__device__ __forceinline__ void silu_mul8(const uint4& g8, const uint4& u8, float2 (&h)[4]) {
+  float2 g[4], u[4];
+  unpack_bf16x8(g8, g);
+  unpack_bf16x8(u8, u);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    h[e] = __fmul2_rn(make_float2(__fdividef(g[e].x, 1.0f + __expf(-g[e].x)), __fdividef(g[e].y, 1.0f + __expf(-g[e].y))), u[e]);
+  const uint32_t top = __vmaxu2(__vimax3_u16x2(g8.x, g8.y, g8.z), g8.w);
+  if (max(top, top << 16) > 0xc2aeffffu) {
+    const auto far = [](float h, float gate, float up) {
+      const float a = __expf(0.5f * gate);
+      return gate < -87.0f ? up * a * gate * a : h;
+    };
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = make_float2(far(h[e].x, g[e].x, u[e].x), far(h[e].y, g[e].y, u[e].y));
+  }
+}
+
 // The warps of one row: 2^SH of them (SH < 0: 2^shift, known at run time), `first` the block's warp they
 // start at.
 template <int SH>
@@ -141,13 +164,7 @@ struct RowPart {
       if constexpr (SRC == kRowBf16) {
         unpack_bf16x8(a[i], v[i]);
       } else if constexpr (SRC == kRowSwiglu) {
-        float2 u[4];
-        unpack_bf16x8(a[i], v[i]);
-        unpack_bf16x8(b[i], u);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          v[i][e] = __fmul2_rn(make_float2(__fdividef(v[i][e].x, 1.0f + __expf(-v[i][e].x)),
-                                           __fdividef(v[i][e].y, 1.0f + __expf(-v[i][e].y))), u[e]);
+        silu_mul8(a[i], b[i], v[i]);
       } else {
         v[i][0] = make_float2(__uint_as_float(a[i].x), __uint_as_float(a[i].y));
         v[i][1] = make_float2(__uint_as_float(a[i].z), __uint_as_float(a[i].w));
