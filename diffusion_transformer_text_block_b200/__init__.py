@@ -273,15 +273,20 @@ def op_ln_modulate(x, shift, scale, stream=None):
 _torch = None
 
 
-def _begin(t, name):
-    """(torch, current device) for a call whose first argument is t."""
+def _load_torch():
     global _torch
     if _torch is None:
         import torch
         _torch = torch
+    return _torch
+
+
+def _begin(t, name):
+    """(torch, current device) for a call whose first argument is t."""
+    torch = _torch or _load_torch()
     if not t.is_cuda:
         raise MossError(1, f"{name} must be a CUDA tensor")
-    return _torch, _torch._C._cuda_getDevice()
+    return torch, torch._C._cuda_getDevice()
 
 
 def _raw_stream(stream, dev):
@@ -320,14 +325,19 @@ def _dtype_code(t, name):
     raise MossError(1, f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
 
 
-def _new(ref, shape, dtype, stream):
-    """A new tensor beside ref, from the pool of the stream that the call runs on (None: the current one)."""
+def _new_on(device, shape, dtype, stream):
+    """A new tensor from the pool of the stream that the call runs on (None: the current one)."""
     if stream is None:
-        return ref.new_empty(shape, dtype=dtype)
+        return _torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, _torch.cuda.Stream):
-        stream = _torch.cuda.ExternalStream(_stream(stream), device=ref.device)
+        stream = _torch.cuda.ExternalStream(_stream(stream), device=device)
     with _torch.cuda.stream(stream):
-        return ref.new_empty(shape, dtype=dtype)
+        return _torch.empty(shape, dtype=dtype, device=device)
+
+
+def _new(ref, shape, dtype, stream):
+    """The same beside ref."""
+    return ref.new_empty(shape, dtype=dtype) if stream is None else _new_on(ref.device, shape, dtype, stream)
 
 
 _INT32_MAX = 0x7fffffff  # the C calls take sizes as 32-bit integers
@@ -485,11 +495,12 @@ def op_qk_norm_rope(q, k, q_gain, k_gain, rope, positions=None, pairing="adjacen
 
 def op_rope_table(grid_h: int, grid_w: int, n_txt: int, stream=None):
     """The model's (cos, sin) for op_qk_norm_rope: CUDA FP32 [grid_h*grid_w + n_txt, 64, 2]."""
-    import torch
+    torch = _load_torch()
     if grid_h < 0 or grid_w < 0 or n_txt < 0:
         raise MossError(1, "grid_h, grid_w and n_txt must be >= 0")
-    table = torch.empty(grid_h * grid_w + n_txt, 64, 2, device="cuda", dtype=torch.float32)
-    _check(lib().moss_op_rope_table(table.data_ptr(), grid_h, grid_w, n_txt, _stream(stream)))
+    dev = torch.cuda.current_device()
+    table = _new_on(torch.device("cuda", dev), (grid_h * grid_w + n_txt, 64, 2), torch.float32, stream)
+    _check(lib().moss_op_rope_table(table.data_ptr(), grid_h, grid_w, n_txt, _raw_stream(stream, dev)))
     return table
 
 

@@ -42,3 +42,59 @@ def test_swiglu_far_gates_beside_others():
     q, scale = moss.op_swiglu_i8(gu)
     assert torch.isnan(scale[:2]).all() and (q[:2] == 0).all()
     assert torch.isfinite(scale[2:]).all() and q[2, 9] == 0
+
+
+# ------------------------------------------------------------------------------ streams
+def every_operator():
+    """name: a call of it with nothing but stream= to fill in; the outputs of each are larger than a megabyte."""
+    x, mod = randn(10, 512, 4096), randn(11, 4096, scale=0.1)
+    gu = randn(12, 512, 8192).bfloat16()
+    a, b = moss.op_quantize_i8(x), moss.op_quantize_i8(randn(13, 4096, 4096))
+    heads, rope = randn(14, 512, 32, 128).bfloat16(), moss.op_rope_table(16, 32, 0)
+    return {"quantize": lambda s: moss.op_quantize_i8(x, stream=s),
+            "ln_modulate": lambda s: moss.op_ln_modulate_i8(x, mod, mod, stream=s),
+            "swiglu": lambda s: moss.op_swiglu_i8(gu, stream=s),
+            "gemm": lambda s: (moss.op_gemm_i8(*a, *b, stream=s),),
+            "qk_norm_rope": lambda s: moss.op_qk_norm_rope(heads, heads, None, None, rope, stream=s),
+            "rope_table": lambda s: (moss.op_rope_table(64, 64, 512, stream=s),)}
+
+
+OPERATORS = ["quantize", "ln_modulate", "swiglu", "gemm", "qk_norm_rope", "rope_table"]
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+@pytest.mark.parametrize("by_handle", [False, True])
+def test_new_tensors_come_from_the_given_streams_pool(name, by_handle):
+    """Blocks of the outputs' sizes lie free in the current stream's pool: work of that stream which is still under
+    way may use them, so a call on another stream must not take them."""
+    call = every_operator()[name]
+    want = call(None)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    spare = [torch.empty_like(w) for w in want for _ in range(3)]
+    free = {t.data_ptr() for t in spare if t.numel() * t.element_size() > 1 << 20}
+    assert free
+    del spare
+    got = call(s.cuda_stream if by_handle else s)
+    torch.cuda.synchronize()
+    assert not free & {g.data_ptr() for g in got}
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+def test_a_call_on_a_given_stream_does_not_wait_for_the_current_one(name):
+    """The current stream is busy for some tenths of a second; the call's stream is done long before."""
+    call = every_operator()[name]
+    s = torch.cuda.Stream()
+    want = [t.clone() for t in call(None)]
+    call(s)  # the stream's pool has its blocks: no allocation below waits for the device
+    torch.cuda.synchronize()
+    busy = torch.cuda.Event()
+    torch.cuda._sleep(600_000_000)
+    busy.record()
+    got = call(s)
+    s.synchronize()
+    done = busy.query()
+    torch.cuda.synchronize()
+    assert not done
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
