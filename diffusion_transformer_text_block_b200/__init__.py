@@ -498,6 +498,10 @@ def op_rope_table(grid_h: int, grid_w: int, n_txt: int, stream=None):
     torch = _load_torch()
     if grid_h < 0 or grid_w < 0 or n_txt < 0:
         raise MossError(1, "grid_h, grid_w and n_txt must be >= 0")
+    if max(grid_h, grid_w, n_txt) > _INT32_MAX:
+        _too_large()
+    if grid_h * grid_w + n_txt > 1 << 24:
+        raise MossError(1, "at most 2^24 tokens")
     dev = torch.cuda.current_device()
     table = _new_on(torch.device("cuda", dev), (grid_h * grid_w + n_txt, 64, 2), torch.float32, stream)
     _check(lib().moss_op_rope_table(table.data_ptr(), grid_h, grid_w, n_txt, _raw_stream(stream, dev)))

@@ -98,3 +98,9 @@ def test_a_call_on_a_given_stream_does_not_wait_for_the_current_one(name):
     torch.cuda.synchronize()
     assert not done
     assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def test_rope_table_sizes():
+    for args in ((1 << 32, 0, 3), (4, 4, 1 << 32), (1 << 12, 1 << 12, 1), (5000, 5000, 0)):
+        with pytest.raises(moss.MossError):
+            moss.op_rope_table(*args)
