@@ -115,6 +115,7 @@ _SIGS = {
     "moss_op_ln_modulate_i8": (_I, [_P, _P, _P, _P, _P, _I, _I, _P]),
     "moss_op_swiglu_i8": (_I, [_P, _I64, _P, _P, _I, _I, _P]),
     "moss_op_gemm_i8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "moss_selftest_gemm_i8_timeout": (_I, [_I, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
     "moss_qk_norm_rope_args_init": (None, [ctypes.POINTER(QkNormRopeArgs), ctypes.c_uint32]),
     "moss_op_qk_norm_rope": (_I, [ctypes.POINTER(QkNormRopeArgs), _P]),
     "moss_op_rope_table": (_I, [_P, _I, _I, _I, _P]),
@@ -424,6 +425,21 @@ def op_gemm_i8(a, a_scale, b, b_scale, bias=None, gate=None, residual=None, out_
         gate if gate is None else _arg(gate, dev, f, (N,), "gate"),
         residual if residual is None else _arg(residual, dev, f, (M, N), "residual"),
         _arg(out, dev, None, (M, N), "out"), _dtype_code(out, "out"), M, N, K, _raw_stream(stream, dev)))
+    return out
+
+
+I8_FAILURES = {"lost load": 1, "lost load, pair": 2, "kept accumulator": 3}
+
+
+def selftest_gemm_i8_timeout(failure: str, a, a_scale, b, b_scale, stream=None):
+    """op_gemm_i8 with one of I8_FAILURES (the failure-path self-test); returns the (meaningless) output tensor."""
+    torch, dev = _begin(a, "a")
+    (M, K), N = a.shape, b.shape[0]
+    out = _new(a, (M, N), torch.bfloat16, stream)
+    _check(lib().moss_selftest_gemm_i8_timeout(
+        I8_FAILURES[failure], _arg(a, dev, torch.int8, (M, K), "a"), _arg(a_scale, dev, torch.float32, (M,), "a_scale"),
+        _arg(b, dev, torch.int8, (N, K), "b"), _arg(b_scale, dev, torch.float32, (N,), "b_scale"), out.data_ptr(), M, N, K,
+        _raw_stream(stream, dev)))
     return out
 
 

@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(kFlatThreads, 1)
         if (!mbar_wait(&empty[stage], phase ^ 1, err, kErrGemmI8Producer, abort_flag)) break;
         armed[stage] = static_cast<int>(phase);
         mbar_arrive_expect_tx(&full[stage], S::kStageBytes);
-        tma_load_2d(sW + stage * S::kWBytes, &tmW, &full[stage], kb * kBK, n0);
+        if (p.selftest != kI8SelftestFlatLoad || blockIdx.x != 0 || kb != kb0)
+          tma_load_2d(sW + stage * S::kWBytes, &tmW, &full[stage], kb * kBK, n0);
         tma_load_2d(sX + stage * S::kXBytes, &tmX, &full[stage], kb * kBK, m0);
         if (++stage == S::kStages) {
           stage = 0;
@@ -517,6 +518,43 @@ constexpr int kPairSmemBytes = kPairStages * kPairStageBytes + 1024 + 256;
 static_assert(kPairSmemBytes <= 227 * 1024, "shared memory");
 constexpr int kPairGroupM = 16;      // M-tiles per band of the tile order
 
+// The warp that waits for the loads and the one that issues the products meet slot by slot at named barrier 1,
+// where both wait; the former says whether a slot failed to fill.
+__device__ __forceinline__ void meet_announcing(bool failed) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %0, 0;\n\t"
+      "bar.red.or.pred q, 1, 64, p;\n\t}" ::"r"(static_cast<uint32_t>(failed))
+      : "memory");
+}
+// The other side: whether the slot is filled.  The calling thread with `issue` set multiplies it (w, x: the
+// slot's descriptors, 32 bytes of K = 2 further each) before the answer is there, which takes longer than the barrier
+// (9216 x 9216 x 3072: 162.4 us, 166.7 with the products behind the answer, in turn).  Products of a slot that failed
+// to fill read what lies there; nothing takes their sums.
+__device__ __forceinline__ bool meet_and_multiply(uint32_t d_tmem, uint64_t w, uint64_t x, uint32_t idesc,
+                                                  uint32_t accumulate, bool issue) {
+  uint32_t failed;
+  asm volatile(
+      "{\n\t.reg .pred none, failed, issue, acc;\n\t"
+      "setp.ne.u32 none, 0, 0;\n\t"
+      "setp.ne.u32 issue, %6, 0;\n\t"
+      "setp.ne.u32 acc, %5, 0;\n\t"
+      "bar.red.or.pred failed, 1, 64, none;\n\t"
+      "tcgen05.fence::after_thread_sync;\n\t"
+      "@issue tcgen05.mma.cta_group::2.kind::i8 [%1], %2, %3, %4, acc;\n\t"
+      "setp.eq.u32 acc, 0, 0;\n\t"
+      "@issue tcgen05.mma.cta_group::2.kind::i8 [%1], %7, %8, %4, acc;\n\t"
+      "@issue tcgen05.mma.cta_group::2.kind::i8 [%1], %9, %10, %4, acc;\n\t"
+      "@issue tcgen05.mma.cta_group::2.kind::i8 [%1], %11, %12, %4, acc;\n\t"
+      "selp.u32 %0, 1, 0, failed;\n\t}"
+      : "=r"(failed)
+      : "r"(d_tmem), "l"(w), "l"(x), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(issue)), "l"(w + 2),
+        "l"(x + 2), "l"(w + 4), "l"(x + 4), "l"(w + 6), "l"(x + 6)
+      : "memory");
+  return failed == 0;
+}
+static_assert(kBK / 32 == 4, "meet_and_multiply issues the products of one slot");
+
 __device__ __forceinline__ void pair_tile(int tile, int num_m, int num_n, int& mb, int& nb) {
   const int band = tile / (kPairGroupM * num_n);
   const int m0 = band * kPairGroupM;
@@ -563,6 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* peer_issued = abort_flag + 1;  // even CTA: slots that the odd one's producer has loaded in all
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -574,6 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int num_n = (p.N + 255) / 256;
   const int num_tiles = num_m * num_n;
   const int num_kb = (p.K + kBK - 1) / kBK;
+  const int pair_slots = (num_tiles - pair + num_pairs - 1) / num_pairs * num_kb;  // of all the pair's tiles
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairStages; ++s) {
@@ -601,6 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync();  // both CTAs' barriers are initialised and their TMEM allocated
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  int issued = 0;  // thread 0: slots loaded
 
   if (warp == 0) {
     if (lane == 0) {
@@ -624,8 +665,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             armed[stage] = static_cast<int>(phase);
             mbar_arrive_expect_tx(&full[stage], 2 * kPairStageBytes);
           }
-          tma_load_2d_pair(sW + stage * kPairOpBytes, &tmW, full_leader, kb * kBK, wrow);
+          if (p.selftest != kI8SelftestPairLoad || blockIdx.x != 0 || issued != 3)
+            tma_load_2d_pair(sW + stage * kPairOpBytes, &tmW, full_leader, kb * kBK, wrow);
           tma_load_2d_pair(sX + stage * kPairOpBytes, &tmX, full_leader, kb * kBK, xrow);
+          ++issued;
           if (++stage == kPairStages) {
             stage = 0;
             phase ^= 1;
@@ -637,8 +680,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     if (leader) {
       // The warp learns of a filled slot by a named barrier, from warp 10: a poll of an mbarrier behind
-      // queued MMAs holds up the next ones (171.8 us for 9216 x 9216 x 3072, 181.9 with polls here).  It
-      // joins every slot's barrier also after a failed wait, so that the arrivals always find it.
+      // queued MMAs holds up the next ones (171.8 us for 9216 x 9216 x 3072, 181.9 with polls here).  Both wait
+      // at that barrier, and both go through every slot also after a failed wait, so neither can meet it twice
+      // without the other.  From a slot that failed to fill on, no slot and no accumulator is handed on: the
+      // producers of both CTAs come to rest, and no epilogue takes the sums.
       constexpr uint32_t kIdesc = idesc_i8(256, 256);
       int stage = 0;
       bool ok = true;
@@ -650,17 +695,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
         for (int kb = 0; kb < num_kb; ++kb) {
-          asm volatile("bar.sync %0, 64;" ::"r"(1 + stage) : "memory");
-          tc_fence_after();
-          if (lane == 0 && ok) {
-            const uint32_t w0 = smem_u32(sW + stage * kPairOpBytes);
-            const uint32_t x0 = smem_u32(sX + stage * kPairOpBytes);
-#pragma unroll
-            for (int k = 0; k < kBK / 32; ++k)
-              mma_i8_ss_pair(d_tmem, sdesc_sw128(w0 + k * 32, 16, 1024), sdesc_sw128(x0 + k * 32, 16, 1024), kIdesc,
-                             (kb | k) != 0 ? 1u : 0u);
-            tc_commit_pair_both(&empty[stage], 0x3);  // the slot in both CTAs
-          }
+          const uint64_t w0 = sdesc_sw128(smem_u32(sW + stage * kPairOpBytes), 16, 1024);
+          const uint64_t x0 = sdesc_sw128(smem_u32(sX + stage * kPairOpBytes), 16, 1024);
+          if (!meet_and_multiply(d_tmem, w0, x0, kIdesc, kb, lane == 0 && ok)) ok = false;
+          if (lane == 0 && ok) tc_commit_pair_both(&empty[stage], 0x3);  // the slot in both CTAs
           __syncwarp();
           if (++stage == kPairStages) stage = 0;
         }
@@ -679,20 +717,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp == 10) {
     if (leader) {
-      // A wait that gives up is recorded and raises the abort flag; the slot is announced all the same and
-      // the kernel runs to its end on what the slots hold.
+      // A wait that gives up is recorded and raises the abort flag; the warps meet for its slot all the same.
       int stage = 0;
       uint32_t phase = 0;
-      for (int tile = pair; tile < num_tiles; tile += num_pairs)
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (lane == 0) mbar_wait(&full[stage], phase, err, kErrGemmI8Mma, abort_flag);
-          __syncwarp();
-          asm volatile("bar.arrive %0, 64;" ::"r"(1 + stage) : "memory");
-          if (++stage == kPairStages) {
-            stage = 0;
-            phase ^= 1;
-          }
+      bool failed = false;
+      for (int i = 0; i < pair_slots; ++i) {
+        if (lane == 0 && !mbar_wait(&full[stage], phase, err, kErrGemmI8Mma, abort_flag)) failed = true;
+        __syncwarp();
+        meet_announcing(failed);
+        if (++stage == kPairStages) {
+          stage = 0;
+          phase ^= 1;
         }
+      }
     }
   } else {
     const int quad = warp & 3;          // TMEM lane quadrant this warp may access
@@ -729,7 +766,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
+      if (lane == 0 && (p.selftest != kI8SelftestPairAccumulator || blockIdx.x != 0 || warp != 2)) {
         if (leader)
           mbar_arrive(&tempty[acc]);
         else
@@ -740,7 +777,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) st_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1), 1);
   cluster_sync();  // the even CTA's MMAs into both TMEMs are complete (drained above)
+  if (*abort_flag) {  // in either CTA, and now in both
+    // The odd CTA may have loaded slots that the even one's producer, which stopped first, never armed (at
+    // most one turn of them, since no slot was given back after that).  They are armed with the odd CTA's
+    // bytes alone and waited for, so that no copy is in flight when a CTA exits.
+    if (!leader && threadIdx.x == 0) st_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(peer_issued)), 0), issued);
+    __syncwarp();
+    cluster_sync();
+    if (leader && threadIdx.x == 0) {
+      const uint64_t t0 = globaltimer_ns();
+      for (int i = issued; i < *peer_issued; ++i) {
+        uint64_t* bar = &full[i % kPairStages];
+        mbar_arrive_expect_tx(bar, kPairStageBytes);
+        while (!mbar_try_wait(smem_u32(bar), (i / kPairStages) & 1) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 512);
@@ -790,6 +847,15 @@ cudaError_t launch_gemm_i8(const int8_t* a, const int8_t* b, const GemmI8Params&
   int split = 1;
   while (split < kMaxSplit && tiles * split * 2 <= num_sms() && split * 2 <= num_kb) split *= 2;
   return launch_flat_nt(nt, a, b, p, split, s, err, emsg);
+}
+
+// Flat kernel: the rule above, a wave of tiles; pairs: three tiles or more for the first pair.
+bool gemm_i8_selftest_reaches(int kind, int M, int N, int K) {
+  if (M <= 16 || K < 256) return false;
+  const int nt = M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  if (kind == kI8SelftestFlatLoad)
+    return static_cast<int64_t>((N - 1) / kTileN + 1) * ((M - 1) / nt + 1) <= num_sms();
+  return static_cast<int64_t>((N - 1) / 256 + 1) * ((M - 1) / 256 + 1) > num_sms() / 2 * 2;
 }
 
 }  // namespace moss

@@ -8,6 +8,9 @@
 
 using namespace moss;
 
+static_assert(kI8SelftestFlatLoad == MOSS_I8_LOST_LOAD && kI8SelftestPairLoad == MOSS_I8_LOST_LOAD_PAIR &&
+              kI8SelftestPairAccumulator == MOSS_I8_KEPT_ACCUMULATOR, "as the header numbers them");
+
 namespace {
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -105,8 +108,9 @@ int moss_op_swiglu_i8(const void* gu, int64_t gu_stride, int8_t* q, float* scale
                                       static_cast<cudaStream_t>(stream)), "swiglu_i8", "");
 }
 
-int moss_op_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale, const void* bias,
-                    const float* gate, const float* residual, void* c, int c_dtype, int M, int N, int K, void* stream) {
+static int gemm_i8_call(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale, const void* bias,
+                        const float* gate, const float* residual, void* c, int c_dtype, int M, int N, int K,
+                        void* stream, int selftest) {
   set_error(MOSS_OK, "");
   if (!known_dtype(c_dtype)) return invalid("c_dtype must be MOSS_DTYPE_F32 or MOSS_DTYPE_BF16");
   if (M < 0 || N < 1 || K < 16 || K % 16 || K > kMaxI8K)
@@ -135,10 +139,25 @@ int moss_op_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, cons
   p.M = M; p.N = N; p.K = K;
   p.a_scale = a_scale; p.b_scale = b_scale; p.bias = static_cast<const bf16*>(bias);
   p.gate = gate; p.residual = residual; p.c = c; p.c_bf16 = c_dtype == MOSS_DTYPE_BF16;
+  p.selftest = selftest;
   std::string detail;
   count_launches(1);
   const cudaError_t e = launch_gemm_i8(a, b, p, static_cast<cudaStream_t>(stream), err, &detail);
   return cuda_status(e, "gemm_i8", detail);
+}
+
+int moss_op_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale, const void* bias,
+                    const float* gate, const float* residual, void* c, int c_dtype, int M, int N, int K, void* stream) {
+  return gemm_i8_call(a, a_scale, b, b_scale, bias, gate, residual, c, c_dtype, M, N, K, stream, 0);
+}
+
+int moss_selftest_gemm_i8_timeout(int failure, const int8_t* a, const float* a_scale, const int8_t* b,
+                                  const float* b_scale, void* c, int M, int N, int K, void* stream) {
+  set_error(MOSS_OK, "");
+  if (failure != MOSS_I8_LOST_LOAD && failure != MOSS_I8_LOST_LOAD_PAIR && failure != MOSS_I8_KEPT_ACCUMULATOR)
+    return invalid("unknown failure");
+  if (M < 1 || N < 1 || !gemm_i8_selftest_reaches(failure, M, N, K)) return invalid("a call of these sizes does not reach the failure");
+  return gemm_i8_call(a, a_scale, b, b_scale, nullptr, nullptr, nullptr, c, MOSS_DTYPE_BF16, M, N, K, stream, failure);
 }
 
 void moss_qk_norm_rope_args_init(moss_qk_norm_rope_args* a, uint32_t struct_size) {

@@ -26,9 +26,13 @@ struct GemmI8Params {
   const float* residual = nullptr;  // [M, N], may be c itself
   void* c = nullptr;                // [M, N] FP32 or BF16
   bool c_bf16 = false;
+  int selftest = 0;                 // 0, or one of the failures below, in the grid's first CTA
 };
+enum : int { kI8SelftestFlatLoad = 1, kI8SelftestPairLoad = 2, kI8SelftestPairAccumulator = 3 };
 cudaError_t launch_gemm_i8(const int8_t* a, const int8_t* b, const GemmI8Params& p, cudaStream_t s, unsigned* err,
                            std::string* emsg);
+// Whether a call of these sizes runs the kernel that this failure is for, far enough to meet it.
+bool gemm_i8_selftest_reaches(int kind, int M, int N, int K);
 
 // Rows to 8-bit integers with one scale a row (dim a multiple of 16, at most kMaxRowDim).
 constexpr int kMaxRowDim = 32768;

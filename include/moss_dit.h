@@ -454,6 +454,18 @@ int moss_op_swiglu_i8(const void* gu, int64_t gu_stride, int8_t* q, float* scale
 int moss_op_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale, const void* bias,
                     const float* gate, const float* residual, void* c, int c_dtype, int M, int N, int K, void* stream);
 
+/* Failure-path self-test of the 8-bit GEMM: moss_op_gemm_i8 with a BF16 c, except that one thing never happens.
+ *   MOSS_I8_LOST_LOAD:         the first CTA never loads its first weights (M > 16 and one wave of tiles)
+ *   MOSS_I8_LOST_LOAD_PAIR:    the first CTA of the first pair never loads the weights of its fourth slot
+ *   MOSS_I8_KEPT_ACCUMULATOR:  a warp of that CTA never hands back an accumulator; the pair's third tile waits
+ *                              for it (the last two: more 256 x 256 tiles than the GPU has SMs)
+ * Bounded waits run out after 2 s, the device error word reads 0x111, 0x112 or 0x113, c is not meaningful, and
+ * every warp of the kernel still finishes; later launches compute normally.  K >= 256.
+ * Errors: as moss_op_gemm_i8; INVALID_ARGUMENT for sizes that do not reach the failure. */
+enum { MOSS_I8_LOST_LOAD = 1, MOSS_I8_LOST_LOAD_PAIR = 2, MOSS_I8_KEPT_ACCUMULATOR = 3 };
+int moss_selftest_gemm_i8_timeout(int failure, const int8_t* a, const float* a_scale, const int8_t* b,
+                                  const float* b_scale, void* c, int M, int N, int K, void* stream);
+
 /* ------------------------------------------------------------------------------------ */
 /* Query/key norm and rotation: what moss_op_attention expects done to q and k.           */
 /* ------------------------------------------------------------------------------------ */

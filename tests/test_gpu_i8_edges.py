@@ -1,9 +1,11 @@
 """The 8-bit linear path where its arithmetic, its sizes and its streams come to their ends, against 64 bits."""
+import time
+
 import pytest
 import torch
 
 import diffusion_transformer_text_block_b200 as moss
-from tests.test_gpu_i8 import check_rows_of, no_device_error, randn, swiglu_reference  # noqa: F401 (a fixture among them)
+from tests.test_gpu_i8 import check_rows_of, gemm_case, no_device_error, randn, swiglu_reference  # noqa: F401 (a fixture among them)
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +106,23 @@ def test_rope_table_sizes():
     for args in ((1 << 32, 0, 3), (4, 4, 1 << 32), (1 << 12, 1 << 12, 1), (5000, 5000, 0)):
         with pytest.raises(moss.MossError):
             moss.op_rope_table(*args)
+
+
+# ------------------------------------------------------------------------------ waits that give up
+@pytest.mark.parametrize("failure,M,N,K", [("lost load", 77, 704, 1024), ("lost load", 300, 300, 256),
+                                           ("lost load, pair", 3840, 3840, 1280), ("kept accumulator", 3840, 3840, 1280),
+                                           ("kept accumulator", 3840, 3840, 256)])
+def test_gemm_wait_gives_up_and_every_warp_finishes(failure, M, N, K):
+    """A load that never comes, or an accumulator that is never handed back: the bounded waits give up (2 s, some
+    of them behind others), the launch ends, and the next launches compute as before."""
+    a, sa, b, sb, *_ = gemm_case(80, M, N, K, False, False)
+    want = moss.op_gemm_i8(a, sa, b, sb)
+    assert moss.device_status(clear=True) == 0
+    t0 = time.time()
+    moss.selftest_gemm_i8_timeout(failure, a, sa, b, sb)
+    status = moss.device_status(clear=True)  # synchronises
+    assert status in (0x111, 0x112, 0x113)
+    assert 1.0 < time.time() - t0 < 60.0
+    for _ in range(2):
+        assert torch.equal(moss.op_gemm_i8(a, sa, b, sb), want)
+        assert moss.device_status(clear=True) == 0
