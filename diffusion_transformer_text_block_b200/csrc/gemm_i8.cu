@@ -51,6 +51,10 @@ constexpr int kFlatThreads = 320;
 constexpr int kMaxSplit = 8;  // portable cluster size
 static_assert(static_cast<int64_t>(kMaxI8K) * 128 * 128 <= (int64_t{1} << 30), "32-bit sums are exact");
 
+// Pieces of `size` that n >= 1 elements fill, for every n of 31 bits.
+__host__ __device__ constexpr int pieces(int n, int size) { return (n - 1) / size + 1; }
+static_assert(pieces(0x7fffffff, 256) == 1 << 23 && pieces(256, 256) == 1 && pieces(257, 256) == 2 && pieces(1, 256) == 1, "");
+
 template <int NT>
 struct FlatShape {
   static constexpr int kWBytes = kTileN * kBK;
@@ -142,12 +146,12 @@ __global__ void __launch_bounds__(kFlatThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int num_n = (p.N + kTileN - 1) / kTileN;
+  const int num_n = pieces(p.N, kTileN);
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int tile = static_cast<int>(blockIdx.x) / split;
   const int n0 = (tile % num_n) * kTileN;
   const int m0 = (tile / num_n) * NT;
-  const int num_kb = (p.K + kBK - 1) / kBK;
+  const int num_kb = pieces(p.K, kBK);
   const int kb0 = static_cast<int>(static_cast<int64_t>(num_kb) * rank / split);
   const int kb1 = static_cast<int>(static_cast<int64_t>(num_kb) * (rank + 1) / split);
 
@@ -323,7 +327,7 @@ cudaError_t launch_flat(const int8_t* a, const int8_t* b, const GemmI8Params& p,
   CUtensorMap tw, tx;
   if (!make_tmap_i8_2d(&tw, b, p.K, p.N, kBK, kTileN, emsg) || !make_tmap_i8_2d(&tx, a, p.K, p.M, kBK, NT, emsg))
     return cudaErrorInvalidValue;
-  const int64_t tiles = static_cast<int64_t>((p.N + kTileN - 1) / kTileN) * ((p.M + NT - 1) / NT);
+  const int64_t tiles = static_cast<int64_t>(pieces(p.N, kTileN)) * pieces(p.M, NT);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
   cfg.blockDim = dim3(kFlatThreads);
@@ -609,10 +613,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1;
   const int num_pairs = gridDim.x >> 1;
-  const int num_m = (p.M + 255) / 256;
-  const int num_n = (p.N + 255) / 256;
+  const int num_m = pieces(p.M, 256);
+  const int num_n = pieces(p.N, 256);
   const int num_tiles = num_m * num_n;
-  const int num_kb = (p.K + kBK - 1) / kBK;
+  const int num_kb = pieces(p.K, kBK);
   const int pair_slots = (num_tiles - pair + num_pairs - 1) / num_pairs * num_kb;  // of all the pair's tiles
 
   if (threadIdx.x == 0) {
@@ -817,7 +821,7 @@ cudaError_t launch_pair(const int8_t* a, const int8_t* b, const GemmI8Params& p,
   CUtensorMap tw, tx;
   if (!make_tmap_i8_2d(&tw, b, p.K, p.N, kBK, 128, emsg) || !make_tmap_i8_2d(&tx, a, p.K, p.M, kBK, 128, emsg))
     return cudaErrorInvalidValue;
-  const int64_t tiles = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + 255) / 256);
+  const int64_t tiles = static_cast<int64_t>(pieces(p.M, 256)) * pieces(p.N, 256);
   const int pairs = static_cast<int>(tiles < num_sms() / 2 ? tiles : num_sms() / 2);
   gemm_i8_pair_kernel<RESID, BF16OUT><<<2 * pairs, kPairThreads, kPairSmemBytes, s>>>(tw, tx, p, err);
   return cudaGetLastError();
@@ -838,12 +842,12 @@ cudaError_t launch_gemm_i8(const int8_t* a, const int8_t* b, const GemmI8Params&
   if (p.M <= 8) return launch_few<1>(a, b, p, s);
   if (p.M <= 16 && p.N <= 8192) return launch_few<2>(a, b, p, s);
   const int nt = p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-  const int64_t tiles = static_cast<int64_t>((p.N + kTileN - 1) / kTileN) * ((p.M + nt - 1) / nt);
+  const int64_t tiles = static_cast<int64_t>(pieces(p.N, kTileN)) * pieces(p.M, nt);
   if (tiles > num_sms()) {
     if (p.residual) return launch_pair<true, false>(a, b, p, s, err, emsg);
     return p.c_bf16 ? launch_pair<false, true>(a, b, p, s, err, emsg) : launch_pair<false, false>(a, b, p, s, err, emsg);
   }
-  const int num_kb = (p.K + kBK - 1) / kBK;
+  const int num_kb = pieces(p.K, kBK);
   int split = 1;
   while (split < kMaxSplit && tiles * split * 2 <= num_sms() && split * 2 <= num_kb) split *= 2;
   return launch_flat_nt(nt, a, b, p, split, s, err, emsg);
@@ -854,8 +858,8 @@ bool gemm_i8_selftest_reaches(int kind, int M, int N, int K) {
   if (M <= 16 || K < 256) return false;
   const int nt = M <= 32 ? 32 : M <= 64 ? 64 : 128;
   if (kind == kI8SelftestFlatLoad)
-    return static_cast<int64_t>((N - 1) / kTileN + 1) * ((M - 1) / nt + 1) <= num_sms();
-  return static_cast<int64_t>((N - 1) / 256 + 1) * ((M - 1) / 256 + 1) > num_sms() / 2 * 2;
+    return static_cast<int64_t>(pieces(N, kTileN)) * pieces(M, nt) <= num_sms();
+  return static_cast<int64_t>(pieces(N, 256)) * pieces(M, 256) > num_sms() / 2 * 2;
 }
 
 }  // namespace moss

@@ -118,7 +118,7 @@ static int gemm_i8_call(const int8_t* a, const float* a_scale, const int8_t* b, 
   if ((gate == nullptr) != (residual == nullptr)) return invalid("gate and residual go together");
   if (residual && c_dtype != MOSS_DTYPE_F32) return invalid("the gated residual form writes FP32");
   if (((static_cast<int64_t>(M) + 15) / 16) * ((static_cast<int64_t>(N) + 127) / 128) * 8 > 0x7fffffff)
-    return invalid("M * N is too large");
+    return invalid("M * N is too large: ceil(M / 16) ceil(N / 128) must be below 2^28");
   const int64_t out = static_cast<int64_t>(M) * N * dtype_bytes(c_dtype);
   if (M == 0) return MOSS_OK;
   if (!a || !a_scale || !b || !b_scale || !c) return invalid("a, a_scale, b, b_scale and c must not be NULL");

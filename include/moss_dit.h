@@ -446,7 +446,8 @@ int moss_op_swiglu_i8(const void* gu, int64_t gu_stride, int8_t* q, float* scale
  *   bias: device BF16 [N] or NULL;  gate: device FP32 [N] and residual: device FP32 [M, N], both or
  *   neither (FP32 c only); residual may be c itself (the update in place)
  *   c: device [M, N] of c_dtype.  a, b, c and residual 16-byte aligned.
- * M >= 0 and N >= 1 of any size, K a multiple of 16 up to 65536 (the sums then fit 32 bits).  The sums
+ * M >= 0 and N >= 1 with ceil(M / 16) ceil(N / 128) < 2^28, each up to 2^31 - 1; K a multiple of 16 up to
+ * 65536 (the sums then fit 32 bits).  The sums
  * are exact; a sum is rounded to FP32 once, scales, bias, gate and residual are applied in FP32, and a
  * BF16 c is rounded once at the end.  c does not depend on how the work is split.
  * Errors: INVALID_ARGUMENT (the above, or c overlaps an input), CUDA.  A device-side wait that gives up

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import diffusion_transformer_text_block_b200 as moss
-from tests.test_gpu_i8 import check_rows_of, gemm_case, no_device_error, randn, swiglu_reference  # noqa: F401 (a fixture among them)
+from tests.test_gpu_i8 import check_gemm, check_rows_of, gemm_case, no_device_error, randn, swiglu_reference  # noqa: F401 (a fixture among them)
 
 pytestmark = pytest.mark.gpu
 
@@ -126,3 +126,25 @@ def test_gemm_wait_gives_up_and_every_warp_finishes(failure, M, N, K):
     for _ in range(2):
         assert torch.equal(moss.op_gemm_i8(a, sa, b, sb), want)
         assert moss.device_status(clear=True) == 0
+
+
+# ------------------------------------------------------------------------------ sizes
+@pytest.mark.parametrize("tokens", [True, False])
+def test_gemm_of_the_largest_size(tokens):
+    """2^31 - 1 tokens by one channel, and one token by as many channels (47 GB each): every output right."""
+    big = 2 ** 31 - 1
+    wide = torch.ones(big, 16, device="cuda", dtype=torch.int8)
+    scale = torch.ones(big, device="cuda")
+    one, unit = torch.ones(1, 16, device="cuda", dtype=torch.int8), torch.ones(1, device="cuda")
+    at = torch.tensor([0, 1, 255, 256, 2 ** 30 + 77, big - 258, big - 257, big - 256, big - 255, big - 2, big - 1], device="cuda")
+    wide[at] = torch.randint(-127, 128, (len(at), 16), generator=torch.Generator("cuda").manual_seed(90), device="cuda",
+                             dtype=torch.int8)
+    scale[at] = 0.5 + torch.arange(len(at), device="cuda")
+    c = moss.op_gemm_i8(wide, scale, one, unit) if tokens else moss.op_gemm_i8(one, unit, wide, scale)
+    c = c.view(-1)
+    check_gemm(c[at][:, None], wide[at], scale[at], one, unit, None, None, None)
+    c[at] = 16.0
+    right = bool((c == 16).all())
+    del c, wide, scale
+    torch.cuda.empty_cache()
+    assert right
