@@ -148,3 +148,18 @@ def test_gemm_of_the_largest_size(tokens):
     del c, wide, scale
     torch.cuda.empty_cache()
     assert right
+
+
+@pytest.mark.parametrize("M,N,K,form", [(9216, 9216, 3072, "bf16"), (4429, 3072, 8192, "resid"), (9216, 3072, 3072, "f32"),
+                                        (5001, 4100, 2688, "bias"), (2304, 9216, 912, "resid")])
+def test_gemm_of_many_tiles_a_pair(M, N, K, form):
+    """Three tiles and more for a CTA pair, each of many K slots (24, 64, 24, 21 and 8 of a ring of 7): both
+    accumulators and every slot are used again and again.  Every output against 64 bits."""
+    args = gemm_case(95, M, N, K, form in ("bias", "resid"), form == "resid")
+    a, sa, b, sb, bias, gate, res = args
+    c = moss.op_gemm_i8(a, sa, b, sb, bias=bias, gate=gate, residual=res,
+                        out_dtype=torch.float32 if form in ("f32", "resid") else torch.bfloat16)
+    assert -(-M // 256) * -(-N // 256) > 2 * 74
+    for r in range(0, M, 1024):
+        rows = slice(r, r + 1024)
+        check_gemm(c[rows], a[rows], sa[rows], b, sb, bias, gate, res[rows] if res is not None else None)
