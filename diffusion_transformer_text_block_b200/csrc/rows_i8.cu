@@ -317,12 +317,12 @@ struct RowArgs {
 };
 
 template <int SRC, int VPL, int SH>
-cudaError_t launch_kernel(const RowArgs& a, int sh, cudaStream_t s, int waves = SRC == kRowBf16 ? 2 : 4) {
+cudaError_t launch_kernel(const RowArgs& a, int sh, cudaStream_t s) {
   const int teams = 8 >> sh;
   // A few waves of blocks that walk over the rows: 2 to 5 % better than one wave, and than a block for
   // every 8 / 2^sh rows.
   const int64_t blocks = (static_cast<int64_t>(a.rows) + teams - 1) / teams;
-  const int64_t most = static_cast<int64_t>(num_sms()) * row_blocks(SRC, VPL) * waves;
+  const int64_t most = static_cast<int64_t>(num_sms()) * row_blocks(SRC, VPL) * (SRC == kRowBf16 ? 2 : 4);
   rows_i8_kernel<SRC, VPL, SH><<<static_cast<unsigned>(blocks < most ? blocks : most), kRowThreads, 0, s>>>(
       a.x, a.x_stride, a.shift, a.mscale, a.q, a.scale, a.rows, a.dim, sh, 1.0f / static_cast<float>(a.dim), a.eps);
   return cudaGetLastError();
