@@ -425,7 +425,8 @@ int moss_op_quantize_i8(const void* x, int x_dtype, int64_t x_stride, int8_t* q,
                         void* stream);
 
 /* moss_op_ln_modulate with its rows made 8-bit: h = LN(x)(1 + scale) + shift in FP32 (eps 1e-6, biased
- * variance), not rounded in between, then q and q_scale from h as in moss_op_quantize_i8.
+ * variance, its squares within FP32's range: |x| up to about 1e18), not rounded in between, then q and
+ * q_scale from h as in moss_op_quantize_i8.
  *   x: device FP32 [rows, dim]; shift, scale: device FP32 [dim]; q: device int8 [rows, dim];
  *   all 16-byte aligned; q_scale: device FP32 [rows].  dim as for moss_op_quantize_i8.
  * Errors: as moss_op_quantize_i8. */
@@ -447,9 +448,10 @@ int moss_op_swiglu_i8(const void* gu, int64_t gu_stride, int8_t* q, float* scale
  *   neither (FP32 c only); residual may be c itself (the update in place)
  *   c: device [M, N] of c_dtype.  a, b, c and residual 16-byte aligned.
  * M >= 0 and N >= 1 with ceil(M / 16) ceil(N / 128) < 2^28, each up to 2^31 - 1; K a multiple of 16 up to
- * 65536 (the sums then fit 32 bits).  The sums
- * are exact; a sum is rounded to FP32 once, scales, bias, gate and residual are applied in FP32, and a
- * BF16 c is rounded once at the end.  c does not depend on how the work is split.
+ * 65536 (the sums then fit 32 bits).  The sums are exact; a sum is rounded to FP32 once, scales, bias, gate
+ * and residual are applied in FP32 in the order written (a sum times its a_scale beyond FP32's range is
+ * infinite, whatever b_scale is), and a BF16 c is rounded once at the end.  c does not depend on how the
+ * work is split.
  * Errors: INVALID_ARGUMENT (the above, or c overlaps an input), CUDA.  A device-side wait that gives up
  * after 2 s sets the device error word (0x111 producer, 0x112 MMA, 0x113 epilogue). */
 int moss_op_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale, const void* bias,
@@ -504,9 +506,10 @@ typedef struct moss_qk_norm_rope_args {
 void moss_qk_norm_rope_args_init(moss_qk_norm_rope_args* args, uint32_t struct_size);
 
 /* y = x * rsqrt(mean(x^2) + eps) * gain over each head, then each pair (a, b) of the first rot_dim
- * elements becomes (a cos - b sin, a sin + b cos); in FP32, rounded once at the end.  A NaN makes its
- * whole head NaN, an infinity its pair NaN and the rest of its head 0.  A token whose position is outside [0, n_pos) is left out
- * (its output is not written) and sets the device error word to 0x401.
+ * elements becomes (a cos - b sin, a sin + b cos); in FP32 (squares too: |x| up to about 1e18), rounded
+ * once at the end.  A NaN makes its whole head NaN, an infinity its pair NaN and the rest of its head 0; with
+ * eps 0 a head whose squares all vanish in FP32 is not finite.  A token whose position is outside [0, n_pos)
+ * is left out (its output is not written) and sets the device error word to 0x401.
  * Errors: ABI_MISMATCH (struct_size), UNSUPPORTED (head_dim), INVALID_ARGUMENT (the rules above), CUDA. */
 int moss_op_qk_norm_rope(const moss_qk_norm_rope_args* args, void* stream);
 
