@@ -507,8 +507,9 @@ void moss_qk_norm_rope_args_init(moss_qk_norm_rope_args* args, uint32_t struct_s
 
 /* y = x * rsqrt(mean(x^2) + eps) * gain over each head, then each pair (a, b) of the first rot_dim
  * elements becomes (a cos - b sin, a sin + b cos); in FP32 (squares too: |x| up to about 1e18), rounded
- * once at the end.  A NaN makes its whole head NaN, an infinity its pair NaN and the rest of its head 0; with
- * eps 0 a head whose squares all vanish in FP32 is not finite.  A token whose position is outside [0, n_pos)
+ * once at the end.  A NaN makes its whole head NaN, an infinity its pair NaN (beyond rot_dim: itself and one of the
+ * eight elements it lies among) and the rest of its head 0; with eps 0 a head whose squares all vanish in FP32
+ * is not finite.  A token whose position is outside [0, n_pos)
  * is left out (its output is not written) and sets the device error word to 0x401.
  * Errors: ABI_MISMATCH (struct_size), UNSUPPORTED (head_dim), INVALID_ARGUMENT (the rules above), CUDA. */
 int moss_op_qk_norm_rope(const moss_qk_norm_rope_args* args, void* stream);
