@@ -8,8 +8,8 @@
 
 using namespace moss;
 
-static_assert(kI8SelftestFlatLoad == MOSS_I8_LOST_LOAD && kI8SelftestPairLoad == MOSS_I8_LOST_LOAD_PAIR &&
-              kI8SelftestPairAccumulator == MOSS_I8_KEPT_ACCUMULATOR, "as the header numbers them");
+static_assert(int{kI8SelftestFlatLoad} == int{MOSS_I8_LOST_LOAD} && int{kI8SelftestPairLoad} == int{MOSS_I8_LOST_LOAD_PAIR} &&
+              int{kI8SelftestPairAccumulator} == int{MOSS_I8_KEPT_ACCUMULATOR}, "as the header numbers them");
 
 namespace {
 
