@@ -17,12 +17,12 @@
 // tile, no barrier before the first load: warps read their channels with 16-byte loads straight into
 // dp4a or mma.sync (the legacy tensor path, which at this rate of bytes is nowhere near its limit;
 // tcgen05 would first have to bring the weights through shared memory).  One token through 9216 x 3072
-// 7.3 us, 3.9 TB/s of weights; the launch and the first loads' latency are 2.5 us of that.
+// 7.5 us, 3.8 TB/s of weights; the launch and the first loads' latency are 2.5 us of that.
 //
 // `gemm_i8_flat_kernel` (a wave of tiles or less): one CTA per tile of 128 output channels and NT tokens
 // (tcgen05.mma kind::i8, 128 x NT x 32), the K axis split over the CTAs of a cluster, whose partial
 // sums meet in shared memory of the cluster (integers: the order does not matter).  Bound by latencies:
-// of 9.5 us for 77 tokens x 3072 x 4096 the first slot is full after 2.2, the weights have streamed
+// of about 9.5 us for 77 tokens x 3072 x 4096 the first slot is full after 2.2, the weights have streamed
 // after 4.6, the sums have met after 6.5 (clocks inside the kernel).
 //   warp 0      TMA producer: 128 x 128 bytes of B and NT x 128 bytes of A per slot (128-byte swizzle)
 //   warp 1      MMA issuer, four 32-deep steps a slot
@@ -31,13 +31,13 @@
 // `gemm_i8_pair_kernel` (more tiles): persistent CTA pairs, 256 channels x 256 tokens a pair
 // (tcgen05.mma.cta_group::2, 256 x 256 x 32) into one of two accumulators, seven 32 KB slots a CTA, the
 // epilogue of a tile under the products of the next.  Bound by the tensor pipe and, in long runs, by the
-// power cap: 9216 x 9216 x 3072 166 us = 3.1 PTOP/s, 8192^3 3.3 PTOP/s, 1.9 to 2.0 times the measured
-// BF16 rate.  (256 x 128 tiles ran at half that rate; two pairs sharing a tile's K gained 6 to 19 % below
+// power cap: 9216 x 9216 x 3072 159 to 166 us = 3.1 to 3.3 PTOP/s, 8192^3 3.3 to 3.4 PTOP/s, 1.9 to 2.1 times
+// the measured BF16 rate.  (256 x 128 tiles ran at half that rate; two pairs sharing a tile's K gained 6 to 19 % below
 // 32 tiles and lost as much above.)
 //   warp 0      TMA producer, in both CTAs, counted on the even CTA's barriers
 //   warp 1      MMA issuer, even CTA only
 //   warps 2..9  epilogue, in both CTAs
-//   warp 10     even CTA: waits for the loads and hands them to warp 1 by named barriers
+//   warp 10     even CTA: waits for the loads and meets warp 1 at a named barrier for each slot
 #include "i8.cuh"
 #include "ops_i8.h"
 
@@ -834,8 +834,8 @@ cudaError_t launch_pair(const int8_t* a, const int8_t* b, const GemmI8Params& p,
 //   2..16         few    8 x 9216 x 3072 7.3 (flat 10.2); from 9 tokens on only up to 8192 channels, since every
 //                        warp reads the tokens again: 16 x 3072 x 3072 5.6 (flat 8.2), 16 x 16384 x 3072 17 (12.8)
 //   one wave of   flat   256 x 3072 x 3072 11.4 (pairs 13.9), 64 x 9216 x 3072 10.8 (12.5); K split while the CTAs stay
-//   tiles or less        one wave: 77 x 3072 x 4096 14.0 / 11.9 / 10.1 / 17.9 for 1 / 2 / 4 / 8 parts (24 to 192 CTAs), 9.5 now for 4
-//   more tiles    pairs  512 x 9216 x 3072 15.2 (flat 25.6), 128 x 32768 x 3072 23.8 (29.9), 20 x 20480 x 3072 22.5 (21.6)
+//   tiles or less        one wave: 77 x 3072 x 4096 14.0 / 11.9 / 10.1 / 17.9 for 1 / 2 / 4 / 8 parts (24 to 192 CTAs), 9.6 to 10.1 now for 4
+//   more tiles    pairs  512 x 9216 x 3072 16 (flat 25.6), 128 x 32768 x 3072 23.8 (29.9), 20 x 20480 x 3072 22.5 (21.6)
 cudaError_t launch_gemm_i8(const int8_t* a, const int8_t* b, const GemmI8Params& p, cudaStream_t s, unsigned* err,
                            std::string* emsg) {
   if (p.M == 1) return launch_one(a, b, p, s);

@@ -329,8 +329,8 @@ cudaError_t launch_kernel(const RowArgs& a, int sh, cudaStream_t s) {
 }
 
 // Rows that fill the lanes exactly have kernels without bounds checks and with constant steps: a third
-// fewer instructions (LayerNorm of 9216 x 3072 33.1 -> 25.6 us, SwiGLU of 9216 x 8192 64.3 -> 58.8 us; with
-// the border check 27.3 = 0.79 and 61.4 us = 0.94 of the HBM rate).
+// fewer instructions (LayerNorm of 9216 x 3072 33.1 -> 25.6 us, SwiGLU of 9216 x 8192 64.3 -> 58.8 us; now, with
+// the border check, 27.2 to 28.7 = 0.75 to 0.79 and 59.7 to 61.2 us = 0.94 to 0.96 of the HBM rate).
 template <int SRC, int VPL>
 cudaError_t launch_shift(const RowArgs& a, int sh, cudaStream_t s) {
   if (a.dim == VPL << (8 + sh)) {
@@ -347,8 +347,8 @@ cudaError_t launch_shift(const RowArgs& a, int sh, cudaStream_t s) {
 template <int SRC>
 cudaError_t launch_rows(const RowArgs& a, cudaStream_t s) {
   const int units = a.dim / 8;
-  // Units a lane where 8 warps or fewer reach that: 12 for BF16 rows (9216 x 3072: 12.4 us with one warp a
-  // row, 14.6 with four), whose registers hold two elements a word; 4 for the others (LayerNorm without the
+  // Units a lane where 8 warps or fewer reach that: 12 for BF16 rows (9216 x 3072 with part of the buffers left
+  // in L2: 12.4 us with one warp a row, 14.6 with four; 14.5 with one where nothing is left), whose registers hold two elements a word; 4 for the others (LayerNorm without the
   // border check: 35 us with one warp, 25.6 with four).  More warps a row while there are too few rows to fill the GPU.
   const int most = SRC == kRowBf16 ? 12 : 4;
   int sh = 0;
